@@ -141,6 +141,33 @@ typedef struct {
     int32_t shared_prefix;   /* 0: [L][2][B][P+N][d]; 1: the shared-prefix layout above */
 } qi21_kv_cache;
 
+/* Prefix K/V cache held in 4 bits: one caller-owned device buffer of
+ * qi21_kv4_cache_bytes(), 4.5 bits an element (28 % of a bf16 cache).
+ *   Format: a group is QI21_KV4_GROUP consecutive dims of one head of one row.
+ *   With a = max |x| of the group, its scale s is 0 if a = 0, else the smallest
+ *   number with a 5-bit significand for which 7 s >= a, kept within [2^-126,
+ *   2^122] and held as bf16; an element is k = rint(x / s) (ties to even) in
+ *   [-7, 7], stored as k + 8. Its value k s has at most 8 significant bits: it is
+ *   exact in bf16 and float32, so the cache has no dtype of its own (one written
+ *   from a float32 cache can be read by a bf16 config). Magnitudes beyond
+ *   7 * 2^122 saturate; a group with a NaN or an infinity stands for NaNs.
+ *   Layout: codes [L][2 (K,V)][batch][H][Pp][Dh/2] bytes (dim 2i in the low half
+ *   of byte i, 2i + 1 in the high half), then scales [L][2][batch][H][Pp][Dh/32]
+ *   bf16; Pp = n_prefix rounded up to QI21_ATTN_KEY_TILE. What the rows behind
+ *   the last one hold never reaches a result.
+ *   prefix_len: device int32 [batch], the rows of each item that exist (clamped
+ *   to 0 .. n_prefix), or NULL: all n_prefix of every item. An item may be empty.
+ * A caller that fills the buffer in this layout by itself sets state to
+ * QI21_CACHE_EXTRACTED. head_dim must be a multiple of QI21_KV4_GROUP. */
+#define QI21_KV4_GROUP 32
+typedef struct {
+    void *base;
+    int32_t *prefix_len;
+    int32_t batch, n_prefix;
+    int32_t n_layers, n_heads, head_dim;
+    int32_t state;
+} qi21_kv4_cache;
+
 /* ---------------------------------------------------------------- host helpers */
 
 /* Packing metadata of a segment list ([2A] §1 build_token_metadata; [LAB] 3A,
@@ -221,6 +248,19 @@ qi21_status qi21_kv_cache_init(qi21_kv_cache *cache, void *base, const qi21_conf
 size_t qi21_kv_cache_bytes_shared(const qi21_config *cfg, int32_t batch, int32_t n_prefix, int32_t n_target);
 qi21_status qi21_kv_cache_init_shared(qi21_kv_cache *cache, void *base, const qi21_config *cfg,
                                       int32_t batch, int32_t n_prefix, int32_t n_target);
+
+/* The 4-bit prefix cache: bytes, and a descriptor over caller memory (state
+ * EMPTY; prefix_len may be NULL). 0 bytes / QI21_ERR_SHAPE or
+ * QI21_ERR_UNSUPPORTED for a config or sizes it cannot hold. */
+size_t qi21_kv4_cache_bytes(const qi21_config *cfg, int32_t batch, int32_t n_prefix);
+qi21_status qi21_kv4_cache_init(qi21_kv4_cache *cache, void *base, const qi21_config *cfg,
+                                int32_t batch, int32_t n_prefix, int32_t *prefix_len);
+/* Workspace of qi21_kv4_attention and qi21_kv4_scores for these sizes (n_tail = 0
+ * for the scores), and of qi21_cached_step_kv4. */
+size_t qi21_kv4_workspace_bytes(const qi21_config *cfg, int32_t batch, int32_t n_q,
+                                int32_t n_prefix, int32_t n_tail);
+size_t qi21_kv4_step_workspace_bytes(const qi21_config *cfg, int32_t batch, int32_t n_prefix,
+                                     int32_t n_target);
 
 /* ---------------------------------------------------------------- device entry points */
 
@@ -390,6 +430,80 @@ qi21_status qi21_denoise_image(const qi21_config *cfg, const qi21_weights *w, qi
                                const double *sigmas, int32_t n_steps, double t_per_sigma, float *x,
                                float *v, float *mod_row_prefix, float *mod_row_target,
                                float *scale_final, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------ the prefix cache in 4 bits */
+
+/* Quantise the prefix rows of every layer of an extracted cache into dst (same
+ * layers, heads and n_prefix; dst->batch = src->batch, or 1 for a shared-prefix
+ * cache). Rows behind an item's prefix_len are neither read nor written. The
+ * target rows of src stay out. src may be freed once the work is done.
+ * On success dst->state = QI21_CACHE_EXTRACTED. */
+qi21_status qi21_kv4_quantize(const qi21_config *cfg, const qi21_kv_cache *src, qi21_kv4_cache *dst,
+                              void *stream);
+
+/* The way back: the values of src, exactly, into the prefix rows of dst in the
+ * config dtype (either layout; sizes as above). Rows behind an item's prefix_len
+ * are left as they are. On success dst->state = QI21_CACHE_EXTRACTED. */
+qi21_status qi21_kv4_dequantize(const qi21_config *cfg, const qi21_kv4_cache *src, qi21_kv_cache *dst,
+                                void *stream);
+
+/* Attention of n_q query rows per item over one layer of a 4-bit cache and over
+ * n_tail further keys in the config dtype (the target's own K/V; n_tail may be 0
+ * and k_tail, v_tail then NULL):
+ *   o_i = sum_j softmax_j(q_i . k_j / sqrt(Dh)) v_j,
+ *   j over the item's prefix rows, then its n_tail tail rows
+ *   q, out [batch][n_q][d], k_tail, v_tail [batch][n_tail][d]   config dtype
+ *   lse    [H][batch][n_q] float32 or NULL: ln sum_j exp(q_i . k_j / sqrt(Dh))
+ * batch = cache->batch, or any batch over a cache of one item (one prefix shared
+ * by every item). A row without any key gets o = 0 and lse = -inf. fp32 scores,
+ * softmax and accumulators; in the BF16 mode the weights are rounded to bf16 for
+ * the product with V. out may not overlap an input. */
+qi21_status qi21_kv4_attention(const qi21_config *cfg, const qi21_kv4_cache *cache, int32_t layer,
+                               const void *q, int32_t batch, int32_t n_q, const void *k_tail,
+                               const void *v_tail, int32_t n_tail, void *out, float *lse,
+                               void *ws, size_t ws_bytes, void *stream);
+
+/* Accumulated attention weight of the prefix rows of one layer:
+ *   scores_out[c][h][j] = scores_in[c][h][j] + sum_i exp(q_i . k_j / sqrt(Dh) - lse_i)
+ * over the n_q query rows of item c; over those of every item where the cache has
+ * one item and batch is larger. scores_in, scores_out [cache->batch][H][n_prefix]
+ * float32; scores_in may be NULL (zeros) or scores_out itself, but may not overlap
+ * it in part. lse as qi21_kv4_attention writes it, so that a query's weights over
+ * its prefix and tail keys sum to 1; a query with lse = -inf adds nothing. Entries
+ * behind an item's prefix_len are copied. The order of the sums is fixed: the same
+ * inputs give the same bits. */
+qi21_status qi21_kv4_scores(const qi21_config *cfg, const qi21_kv4_cache *cache, int32_t layer,
+                            const void *q, int32_t batch, int32_t n_q, const float *lse,
+                            const float *scores_in, float *scores_out, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* Keep the `keep` rows of the largest scores of every (layer, item, head) and
+ * write them, in their order, as the rows of dst (dst->n_prefix = keep, same
+ * layers, heads and batch; its buffer may not overlap src's). K is stored after
+ * RoPE, so a kept row keeps its position.
+ *   scores [L][batch][H][n_prefix] float32; rows [0, n_protected) are kept first
+ *   (the text, say), then larger scores before smaller ones, equal scores in the
+ *   order of the rows; a NaN score comes last.
+ *   kept [L][batch][H][keep] int32: the rows kept, ascending
+ * An item with fewer than `keep` rows keeps all it has: kept is -1 behind them and
+ * those rows of dst are left as they are. min(keep, length) is written to
+ * dst->prefix_len where that is not NULL; it must be given where src has lengths.
+ * On success dst->state = QI21_CACHE_EXTRACTED. */
+qi21_status qi21_kv4_evict(const qi21_config *cfg, const qi21_kv4_cache *src, const float *scores,
+                           int32_t keep, int32_t n_protected, qi21_kv4_cache *dst, int32_t *kept,
+                           void *stream);
+
+/* qi21_cached_step with the prefix read from a 4-bit cache. The step's target K/V
+ * live in the workspace (qi21_kv4_step_workspace_bytes), so nothing of the
+ * extracted cache is needed. batch items of n_target tokens; the cache has batch
+ * items, or one that all share. Buffers as in qi21_cached_step.
+ *   scores [L][cache->batch][H][n_prefix] float32 or NULL: every layer's attention
+ *   weight of this step is added to it (the input of qi21_kv4_evict). */
+qi21_status qi21_cached_step_kv4(const qi21_config *cfg, const qi21_weights *w,
+                                 const qi21_kv4_cache *cache, int32_t batch, int32_t n_target,
+                                 const float *x_k, const float *cos_sin_target,
+                                 const float *mod_row_target, const float *scale_final, float *v_out,
+                                 float *scores, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronise the stream, then read and clear the device error word of the
  * workspace. Returns QI21_OK, QI21_ERR_DEVICE_TIMEOUT, QI21_ERR_DEVICE_CHECK or

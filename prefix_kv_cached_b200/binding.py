@@ -66,6 +66,12 @@ class qi21_kv_cache(ct.Structure):
                 ("dtype", ct.c_int32), ("state", ct.c_int32), ("shared_prefix", ct.c_int32)]
 
 
+class qi21_kv4_cache(ct.Structure):
+    _fields_ = [("base", ct.c_void_p), ("prefix_len", ct.c_void_p), ("batch", ct.c_int32),
+                ("n_prefix", ct.c_int32), ("n_layers", ct.c_int32), ("n_heads", ct.c_int32),
+                ("head_dim", ct.c_int32), ("state", ct.c_int32)]
+
+
 class qi21_kernel_time(ct.Structure):
     _fields_ = [("name", ct.c_char_p), ("launches", ct.c_int64), ("total_ms", ct.c_double)]
 
@@ -110,6 +116,22 @@ _SIGS = {
     "qi21_euler_update_at": (_I32, [_P, _P, _P, _I32, _P, ct.c_int64, _P]),
     "qi21_denoise_image": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_weights), ct.POINTER(qi21_kv_cache),
                                   _P, _P, _P, _P, _P, _I32, ct.c_double, _P, _P, _P, _P, _P, _P, ct.c_size_t, _P]),
+    "qi21_kv4_cache_bytes": (ct.c_size_t, [ct.POINTER(qi21_config), _I32, _I32]),
+    "qi21_kv4_cache_init": (_I32, [ct.POINTER(qi21_kv4_cache), _P, ct.POINTER(qi21_config), _I32, _I32, _P]),
+    "qi21_kv4_workspace_bytes": (ct.c_size_t, [ct.POINTER(qi21_config), _I32, _I32, _I32, _I32]),
+    "qi21_kv4_step_workspace_bytes": (ct.c_size_t, [ct.POINTER(qi21_config), _I32, _I32, _I32]),
+    "qi21_kv4_quantize": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_kv_cache), ct.POINTER(qi21_kv4_cache),
+                                 _P]),
+    "qi21_kv4_dequantize": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_kv4_cache), ct.POINTER(qi21_kv_cache),
+                                   _P]),
+    "qi21_kv4_attention": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_kv4_cache), _I32, _P, _I32, _I32, _P, _P,
+                                  _I32, _P, _P, _P, ct.c_size_t, _P]),
+    "qi21_kv4_scores": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_kv4_cache), _I32, _P, _I32, _I32, _P, _P, _P,
+                               _P, ct.c_size_t, _P]),
+    "qi21_kv4_evict": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_kv4_cache), _P, _I32, _I32,
+                              ct.POINTER(qi21_kv4_cache), _P, _P]),
+    "qi21_cached_step_kv4": (_I32, [ct.POINTER(qi21_config), ct.POINTER(qi21_weights), ct.POINTER(qi21_kv4_cache),
+                                    _I32, _I32, _P, _P, _P, _P, _P, _P, _P, ct.c_size_t, _P]),
     "qi21_check_device_error": (_I32, [_P, ct.c_size_t, _P]),
     "qi21_status_string": (ct.c_char_p, [_I32]),
     "qi21_selftest_wait_timeout": (_I32, [_P, ct.c_size_t, ct.c_int64, _P]),
@@ -337,6 +359,55 @@ def qi21_denoise_image(cfg, weights, cache, prefix_hidden, cos_sin_prefix, kv_li
                                   _addr(sigmas), int(n_steps), float(t_per_sigma), _addr(x), _addr(v),
                                   _addr(mod_row_prefix), _addr(mod_row_target), _addr(scale_final), _addr(ws),
                                   ws_bytes, stream)
+
+
+def qi21_kv4_cache_bytes(cfg, batch, n_prefix):
+    return lib.qi21_kv4_cache_bytes(ct.byref(cfg), batch, n_prefix)
+
+
+def qi21_kv4_cache_init(base, cfg, batch, n_prefix, prefix_len=None):
+    cache = qi21_kv4_cache()
+    check("qi21_kv4_cache_init", lib.qi21_kv4_cache_init(ct.byref(cache), _addr(base), ct.byref(cfg), batch,
+                                                         n_prefix, _addr(prefix_len)))
+    return cache
+
+
+def qi21_kv4_workspace_bytes(cfg, batch, n_q, n_prefix, n_tail=0):
+    return lib.qi21_kv4_workspace_bytes(ct.byref(cfg), batch, n_q, n_prefix, n_tail)
+
+
+def qi21_kv4_step_workspace_bytes(cfg, batch, n_prefix, n_target):
+    return lib.qi21_kv4_step_workspace_bytes(ct.byref(cfg), batch, n_prefix, n_target)
+
+
+def qi21_kv4_quantize(cfg, cache, cache4, stream=0):
+    return lib.qi21_kv4_quantize(ct.byref(cfg), ct.byref(cache), ct.byref(cache4), stream)
+
+
+def qi21_kv4_dequantize(cfg, cache4, cache, stream=0):
+    return lib.qi21_kv4_dequantize(ct.byref(cfg), ct.byref(cache4), ct.byref(cache), stream)
+
+
+def qi21_kv4_attention(cfg, cache4, layer, q, batch, n_q, k_tail, v_tail, n_tail, out, lse, ws, ws_bytes, stream=0):
+    return lib.qi21_kv4_attention(ct.byref(cfg), ct.byref(cache4), layer, _addr(q), batch, n_q, _addr(k_tail),
+                                  _addr(v_tail), n_tail, _addr(out), _addr(lse), _addr(ws), ws_bytes, stream)
+
+
+def qi21_kv4_scores(cfg, cache4, layer, q, batch, n_q, lse, scores_in, scores_out, ws, ws_bytes, stream=0):
+    return lib.qi21_kv4_scores(ct.byref(cfg), ct.byref(cache4), layer, _addr(q), batch, n_q, _addr(lse),
+                               _addr(scores_in), _addr(scores_out), _addr(ws), ws_bytes, stream)
+
+
+def qi21_kv4_evict(cfg, cache4, scores, keep, n_protected, cache4_out, kept, stream=0):
+    return lib.qi21_kv4_evict(ct.byref(cfg), ct.byref(cache4), _addr(scores), keep, n_protected,
+                              ct.byref(cache4_out), _addr(kept), stream)
+
+
+def qi21_cached_step_kv4(cfg, weights, cache4, batch, n_target, x_k, cos_sin_target, mod_row_target, scale_final,
+                         v_out, scores, ws, ws_bytes, stream=0):
+    return lib.qi21_cached_step_kv4(ct.byref(cfg), ct.byref(weights), ct.byref(cache4), batch, n_target, _addr(x_k),
+                                    _addr(cos_sin_target), _addr(mod_row_target), _addr(scale_final), _addr(v_out),
+                                    _addr(scores), _addr(ws), ws_bytes, stream)
 
 
 def qi21_check_device_error(ws, ws_bytes, stream=0):

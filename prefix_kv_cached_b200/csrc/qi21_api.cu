@@ -325,6 +325,10 @@ static bool build_tc_maps(TcMaps &t, const qi21_config &c, const qi21_weights &w
     return ok;
 }
 
+}  // namespace qi21
+#include "qi21_kv4_api.cuh"
+namespace qi21 {
+
 // ------------------------------------------------------------------ block stack
 struct StackArgs {
     int B, M, split;          // items, rows per item in this call, rows < split read the prefix row
@@ -347,6 +351,12 @@ struct StackArgs {
     // item b's target rows start at Pp + b*N (kv_bstride = N*d, row_off = Pp)
     bool shared;
     int shared_P, shared_Pp;
+    // 4-bit prefix cache (cached step): the K/V buffer above holds the target rows
+    // alone, and the attention reads the prefix from here; kv4_scores [L][items][H][P]
+    // or null receives every layer's attention weights
+    const qi21_kv4_cache *kv4;
+    float *kv4_scores, *kv4_lse;
+    char *kv4_ws;
 };
 
 template <typename T>
@@ -476,7 +486,14 @@ static void run_stack(Launcher &L, const qi21_config &c, const qi21_weights &w, 
         }
         if (a.kv_only_last && l == c.n_layers - 1) break;
 
-        if (tc) {
+        if (a.kv4) {
+            launch_kv4_attention<T>(L, c, *a.kv4, l, a.q, a.B, a.M, kdst, vdst, a.M, a.o,
+                                    a.kv4_scores ? a.kv4_lse : nullptr, a.kv4_ws, a.err);
+            if (a.kv4_scores) {
+                float *sc = a.kv4_scores + (size_t)l * a.kv4->batch * H * a.kv4->n_prefix;
+                launch_kv4_scores<T>(L, c, *a.kv4, l, a.q, a.B, a.M, a.kv4_lse, sc, sc, a.kv4_ws, a.err);
+            }
+        } else if (tc) {
             AttnParams ap{};
             ap.Mq = a.M;
             ap.kv_len = a.kv_len;
@@ -656,6 +673,26 @@ static void launch_final(Launcher &L, const qi21_config &c, const float *h, int 
         k_final<T><<<(rows + 3) / 4, 256, smem, L.st>>>(h, M, off, N, d, sf, (const T *)w_out, c.latent_ch, c.ln_eps,
                                                        v, rows);
     });
+}
+
+// The cached step of the target rows once its arguments are laid out: img_in, the
+// blocks, the final AdaLN and proj_out.
+static void run_target_step(Launcher &L, const qi21_config &c, const qi21_weights &w, const StackArgs &a,
+                            const WsLayout &lay, const float *x_k, const float *scale_final, float *v_out, char *wsb) {
+    const int B = a.B, N = a.M;
+    if (c.dtype == QI21_DTYPE_BF16 && tc_head_supported(c)) {
+        launch_img_in_tc(L, c, x_k, w.w_img_in, a.h, B * N, (bf16 *)(wsb + lay.xin), a.err);
+        run_stack<bf16>(L, c, w, a);
+        launch_final_tc(L, c, a.h, B * N, scale_final, w.w_out, v_out, wsb, lay, a.err);
+    } else if (c.dtype == QI21_DTYPE_BF16) {
+        launch_img_in<bf16>(L, c, x_k, w.w_img_in, a.h, B, N, N, 0);
+        run_stack<bf16>(L, c, w, a);
+        launch_final<bf16>(L, c, a.h, N, 0, B, N, scale_final, w.w_out, v_out);
+    } else {
+        launch_img_in<float>(L, c, x_k, w.w_img_in, a.h, B, N, N, 0);
+        run_stack<float>(L, c, w, a);
+        launch_final<float>(L, c, a.h, N, 0, B, N, scale_final, w.w_out, v_out);
+    }
 }
 
 // ------------------------------------------------------------------ validation helpers
@@ -878,20 +915,154 @@ extern "C" qi21_status qi21_cached_step(const qi21_config *c, const qi21_weights
     }
     a.kv_limit = nullptr;
     a.kv_only_last = false;
-    if (c->dtype == QI21_DTYPE_BF16 && tc_head_supported(*c)) {
-        launch_img_in_tc(L, *c, x_k, w->w_img_in, a.h, B * N, (bf16 *)(wsb + lay.xin), a.err);
-        run_stack<bf16>(L, *c, *w, a);
-        launch_final_tc(L, *c, a.h, B * N, scale_final, w->w_out, v_out, wsb, lay, a.err);
-    } else if (c->dtype == QI21_DTYPE_BF16) {
-        launch_img_in<bf16>(L, *c, x_k, w->w_img_in, a.h, B, N, N, 0);
-        run_stack<bf16>(L, *c, *w, a);
-        launch_final<bf16>(L, *c, a.h, N, 0, B, N, scale_final, w->w_out, v_out);
-    } else {
-        launch_img_in<float>(L, *c, x_k, w->w_img_in, a.h, B, N, N, 0);
-        run_stack<float>(L, *c, *w, a);
-        launch_final<float>(L, *c, a.h, N, 0, B, N, scale_final, w->w_out, v_out);
-    }
+    run_target_step(L, *c, *w, a, lay, x_k, scale_final, v_out, wsb);
     return finish(L);
+}
+
+extern "C" qi21_status qi21_cached_step_kv4(const qi21_config *c, const qi21_weights *w, const qi21_kv4_cache *cache,
+                                            int32_t B, int32_t N, const float *x_k, const float *cos_sin_target,
+                                            const float *mod_row_target, const float *scale_final, float *v_out,
+                                            float *scores, void *ws, size_t ws_bytes, void *stream) {
+    qi21_status s = check_shapes(c);
+    if (s) return s;
+    if ((s = check_weights(w, false))) return s;
+    if ((s = check_kv4_queries(c, cache, B, N, N))) return s;
+    if (!al16(x_k) || !al16(cos_sin_target) || !al16(mod_row_target) || !al16(scale_final) || !al16(v_out) ||
+        ((uintptr_t)scores & 15) || !al16(ws))
+        return QI21_ERR_INVALID_ARG;
+    const WsLayout lay = ws_layout(*c, B, 0, N);
+    const Kv4StepLayout k4 = kv4_step_layout(*c, B, cache->n_prefix, N);
+    if (ws_bytes < k4.total) return QI21_ERR_WORKSPACE_TOO_SMALL;
+    char *wsb = (char *)ws;
+    Launcher L((cudaStream_t)stream);
+    const int d = c->d_model;
+    StackArgs a{};
+    a.B = B; a.M = N; a.split = 0; a.P = 0; a.N = N;
+    a.h = (float *)(wsb + lay.h);
+    a.xn = wsb + lay.xn; a.q = wsb + lay.q; a.o = wsb + lay.o; a.hid = wsb + lay.hid;
+    a.gemm = (float *)(wsb + lay.gemm); a.gates = (float *)(wsb + lay.gates); a.err = (uint32_t *)(wsb + lay.err);
+    a.mod_lo = mod_row_target; a.mod_hi = mod_row_target;
+    a.cos_sin = cos_sin_target;
+    a.kv_k0 = wsb + lay.kvf;                   // target K, V [B][N][d], every layer's in turn
+    a.kv_v0 = wsb + lay.kvf + dtype_bytes(c->dtype) * (size_t)B * N * d;
+    a.kv_layer_stride = 0;
+    a.kv_bstride = (int64_t)N * d;
+    a.row_off = 0;
+    a.kv_len = N;
+    a.kv4 = cache;
+    a.kv4_scores = scores;
+    a.kv4_lse = (float *)(wsb + k4.lse);
+    a.kv4_ws = wsb + k4.kv4;
+    run_target_step(L, *c, *w, a, lay, x_k, scale_final, v_out, wsb);
+    return finish(L);
+}
+
+static qi21_status check_kv4_pair(const qi21_config *c, const qi21_kv_cache *a, const qi21_kv4_cache *k) {
+    qi21_status s = check_shapes(c);
+    if (s) return s;
+    if ((s = check_kv4(c, k))) return s;
+    if (!a || !al16(a->base)) return QI21_ERR_INVALID_ARG;
+    return kv4_matches(c, a, k) ? QI21_OK : QI21_ERR_CACHE_STATE;
+}
+
+extern "C" qi21_status qi21_kv4_quantize(const qi21_config *c, const qi21_kv_cache *src, qi21_kv4_cache *dst,
+                                         void *stream) {
+    qi21_status s = check_kv4_pair(c, src, dst);
+    if (s) return s;
+    if (src->state != QI21_CACHE_EXTRACTED) return QI21_ERR_CACHE_STATE;
+    dst->state = QI21_CACHE_EMPTY;
+    Launcher L((cudaStream_t)stream);
+    if (c->dtype == QI21_DTYPE_BF16) launch_kv4_quantize<bf16>(L, *c, *src, *dst);
+    else launch_kv4_quantize<float>(L, *c, *src, *dst);
+    s = finish(L);
+    if (s == QI21_OK) dst->state = QI21_CACHE_EXTRACTED;
+    return s;
+}
+
+extern "C" qi21_status qi21_kv4_dequantize(const qi21_config *c, const qi21_kv4_cache *src, qi21_kv_cache *dst,
+                                           void *stream) {
+    qi21_status s = check_kv4_pair(c, dst, src);
+    if (s) return s;
+    if (src->state != QI21_CACHE_EXTRACTED) return QI21_ERR_CACHE_STATE;
+    dst->state = QI21_CACHE_EMPTY;
+    Launcher L((cudaStream_t)stream);
+    if (c->dtype == QI21_DTYPE_BF16) launch_kv4_dequantize<bf16>(L, *c, *src, *dst);
+    else launch_kv4_dequantize<float>(L, *c, *src, *dst);
+    s = finish(L);
+    if (s == QI21_OK) dst->state = QI21_CACHE_EXTRACTED;
+    return s;
+}
+
+extern "C" qi21_status qi21_kv4_attention(const qi21_config *c, const qi21_kv4_cache *cache, int32_t layer,
+                                          const void *q, int32_t B, int32_t n_q, const void *k_tail,
+                                          const void *v_tail, int32_t n_tail, void *out, float *lse, void *ws,
+                                          size_t ws_bytes, void *stream) {
+    qi21_status s = check_shapes(c);
+    if (s) return s;
+    if ((s = check_kv4_queries(c, cache, B, n_q, n_tail))) return s;
+    if (layer < 0 || layer >= c->n_layers || !al16(q) || !al16(out) || ((uintptr_t)lse & 15) || !al16(ws) ||
+        (n_tail > 0 && (!al16(k_tail) || !al16(v_tail))))
+        return QI21_ERR_INVALID_ARG;
+    if (ws_bytes < kv4_plan(*c, B, n_q, cache->n_prefix, n_tail).total) return QI21_ERR_WORKSPACE_TOO_SMALL;
+    Launcher L((cudaStream_t)stream);
+    if (c->dtype == QI21_DTYPE_BF16)
+        launch_kv4_attention<bf16>(L, *c, *cache, layer, q, B, n_q, k_tail, v_tail, n_tail, out, lse, (char *)ws,
+                                   (uint32_t *)ws);
+    else
+        launch_kv4_attention<float>(L, *c, *cache, layer, q, B, n_q, k_tail, v_tail, n_tail, out, lse, (char *)ws,
+                                    (uint32_t *)ws);
+    return finish(L);
+}
+
+extern "C" qi21_status qi21_kv4_scores(const qi21_config *c, const qi21_kv4_cache *cache, int32_t layer, const void *q,
+                                       int32_t B, int32_t n_q, const float *lse, const float *scores_in,
+                                       float *scores_out, void *ws, size_t ws_bytes, void *stream) {
+    qi21_status s = check_shapes(c);
+    if (s) return s;
+    if ((s = check_kv4_queries(c, cache, B, n_q, 0))) return s;
+    if (layer < 0 || layer >= c->n_layers || !al16(q) || !al16(lse) || ((uintptr_t)scores_in & 15) ||
+        !al16(scores_out) || !al16(ws))
+        return QI21_ERR_INVALID_ARG;
+    if (ws_bytes < kv4_plan(*c, B, n_q, cache->n_prefix, 0).total) return QI21_ERR_WORKSPACE_TOO_SMALL;
+    Launcher L((cudaStream_t)stream);
+    if (c->dtype == QI21_DTYPE_BF16)
+        launch_kv4_scores<bf16>(L, *c, *cache, layer, q, B, n_q, lse, scores_in, scores_out, (char *)ws,
+                                (uint32_t *)ws);
+    else
+        launch_kv4_scores<float>(L, *c, *cache, layer, q, B, n_q, lse, scores_in, scores_out, (char *)ws,
+                                 (uint32_t *)ws);
+    return finish(L);
+}
+
+extern "C" qi21_status qi21_kv4_evict(const qi21_config *c, const qi21_kv4_cache *src, const float *scores,
+                                      int32_t keep, int32_t n_protected, qi21_kv4_cache *dst, int32_t *kept,
+                                      void *stream) {
+    qi21_status s = check_shapes(c);
+    if (s) return s;
+    if ((s = check_kv4(c, src)) || (s = check_kv4(c, dst))) return s;
+    if (!al16(scores) || !al16(kept) || (src->prefix_len && !dst->prefix_len)) return QI21_ERR_INVALID_ARG;
+    if (keep < 1 || keep > src->n_prefix || n_protected < 0 || n_protected > keep) return QI21_ERR_SHAPE;
+    if (src->state != QI21_CACHE_EXTRACTED || dst->batch != src->batch || dst->n_prefix != keep)
+        return QI21_ERR_CACHE_STATE;
+    const char *a = (const char *)src->base, *b = (const char *)dst->base;
+    const size_t an = qi21_kv4_cache_bytes(c, src->batch, src->n_prefix), bn = qi21_kv4_cache_bytes(c, dst->batch, keep);
+    if (a < b + bn && b < a + an) return QI21_ERR_INVALID_ARG;       // the gather is not in place
+    if (src->prefix_len && src->prefix_len == dst->prefix_len) return QI21_ERR_INVALID_ARG;
+    dst->state = QI21_CACHE_EMPTY;
+    Launcher L((cudaStream_t)stream);
+    const Kv4Dims cd = kv4_dims(*src), od = kv4_dims(*dst);
+    L.run("kv4_select", [&] {
+        k_kv4_select<<<dim3(cd.H, cd.B, c->n_layers), KV4_SEL_THREADS, 0, L.st>>>(scores, cd, src->prefix_len, keep,
+                                                                                n_protected, kept, dst->prefix_len);
+    });
+    L.run("kv4_gather", [&] {
+        const int64_t pieces = (int64_t)keep * (cd.Dh / KV4_GROUP);
+        k_kv4_gather<<<dim3((unsigned)((pieces + 255) / 256), cd.H, c->n_layers * cd.B), 256, 0, L.st>>>(
+            (const uint8_t *)src->base, cd, kept, keep, (uint8_t *)dst->base, od);
+    });
+    s = finish(L);
+    if (s == QI21_OK) dst->state = QI21_CACHE_EXTRACTED;
+    return s;
 }
 
 extern "C" qi21_status qi21_full_recompute_step(const qi21_config *c, const qi21_weights *w, int32_t B, int32_t P,

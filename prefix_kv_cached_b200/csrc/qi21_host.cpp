@@ -245,3 +245,36 @@ extern "C" qi21_status qi21_kv_cache_init_shared(qi21_kv_cache *cache, void *bas
     if (s == QI21_OK) cache->shared_prefix = 1;
     return s;
 }
+
+extern "C" size_t qi21_kv4_cache_bytes(const qi21_config *c, int32_t B, int32_t P) {
+    if (!qi21_config_ok(c) || !qi21::kv4_head_dim_ok(*c) || B <= 0 || P <= 0) return 0;
+    const size_t rows = (size_t)c->n_layers * 2 * B * c->n_heads * (size_t)padded_prefix(P);
+    return rows * (c->head_dim / 2) + rows * (c->head_dim / QI21_KV4_GROUP) * 2;
+}
+
+extern "C" qi21_status qi21_kv4_cache_init(qi21_kv4_cache *cache, void *base, const qi21_config *c, int32_t B,
+                                           int32_t P, int32_t *prefix_len) {
+    if (!cache || !base || !qi21_config_ok(c)) return QI21_ERR_INVALID_ARG;
+    if ((((uintptr_t)base) & 15) || (((uintptr_t)prefix_len) & 15)) return QI21_ERR_INVALID_ARG;
+    if (!qi21::kv4_head_dim_ok(*c)) return QI21_ERR_UNSUPPORTED;
+    if (B <= 0 || P <= 0) return QI21_ERR_SHAPE;
+    cache->base = base;
+    cache->prefix_len = prefix_len;
+    cache->batch = B;
+    cache->n_prefix = P;
+    cache->n_layers = c->n_layers;
+    cache->n_heads = c->n_heads;
+    cache->head_dim = c->head_dim;
+    cache->state = QI21_CACHE_EMPTY;
+    return QI21_OK;
+}
+
+extern "C" size_t qi21_kv4_workspace_bytes(const qi21_config *c, int32_t B, int32_t n_q, int32_t P, int32_t n_tail) {
+    if (!qi21_config_ok(c) || !qi21::kv4_head_dim_ok(*c) || B <= 0 || n_q <= 0 || P <= 0 || n_tail < 0) return 0;
+    return qi21::kv4_plan(*c, B, n_q, P, n_tail).total;
+}
+
+extern "C" size_t qi21_kv4_step_workspace_bytes(const qi21_config *c, int32_t B, int32_t P, int32_t N) {
+    if (!qi21_config_ok(c) || !qi21::kv4_head_dim_ok(*c) || B <= 0 || P <= 0 || N <= 0) return 0;
+    return qi21::kv4_step_layout(*c, B, P, N).total;
+}

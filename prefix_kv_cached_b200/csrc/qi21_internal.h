@@ -95,4 +95,46 @@ inline WsLayout ws_layout(const qi21_config &c, int64_t B, int64_t P, int64_t N)
     return L;
 }
 
+// Plan of an attention over a 4-bit cache: how the keys are split, and the fp32
+// partial results (log2-sum-exp, then normalised outputs) in the workspace. Host
+// arithmetic on sizes alone, so that the size query and the call agree.
+struct Kv4Plan {
+    int n_split;
+    size_t err, part_l, part_o, total;
+};
+
+inline Kv4Plan kv4_plan(const qi21_config &c, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
+    Kv4Plan p{};
+    const int64_t keys = P + n_tail, H = c.n_heads;
+    // CUDA-core kernel: CTAs of 32 query rows; two CTAs an SM of 148, at least 64 keys each
+    const int64_t ctas = (n_q + 31) / 32 * H * B;
+    int64_t n = (2 * 148 + ctas - 1) / ctas;
+    if (n > (keys + 63) / 64) n = (keys + 63) / 64;
+    p.n_split = (int)(n < 1 ? 1 : n);
+    const size_t rows = p.n_split > 1 ? (size_t)(B * H * n_q) * p.n_split : 0;
+    p.part_l = 256;
+    p.part_o = p.part_l + align256(rows * 4);
+    p.total = p.part_o + align256(rows * 4 * c.head_dim);
+    return p;
+}
+
+// Workspace of the cached step over a 4-bit cache: that of a cached step without
+// prefix (its full-recompute K/V region holds the target K/V), the rows'
+// log-sum-exps, and the attention's partial results.
+struct Kv4StepLayout {
+    size_t lse, kv4, total;
+};
+
+inline Kv4StepLayout kv4_step_layout(const qi21_config &c, int64_t B, int64_t P, int64_t N) {
+    Kv4StepLayout s{};
+    s.lse = ws_layout(c, B, 0, N).total;
+    s.kv4 = s.lse + align256(sizeof(float) * (size_t)c.n_heads * B * N);
+    s.total = s.kv4 + kv4_plan(c, B, N, P, N).total;
+    return s;
+}
+
+inline bool kv4_head_dim_ok(const qi21_config &c) {
+    return c.head_dim % QI21_KV4_GROUP == 0 && c.head_dim <= 128;
+}
+
 }  // namespace qi21

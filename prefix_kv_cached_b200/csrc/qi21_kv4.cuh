@@ -1,0 +1,619 @@
+// Prefix K/V cache held in 4 bits: the format, the kernels that write it, read
+// it back and evict rows from it, and the CUDA-core forms of the attention over
+// it and of the accumulated attention weight (the F32 mode).
+//
+// Format. A group is 32 consecutive dims of one head of one row. With
+// a = max |x| of the group, its scale s is 0 if a = 0, else the smallest number
+// with a 5-bit significand for which 7 s >= a (kept in [2^-126, 2^122], held as
+// bf16); an element is k = rint(x / s), ties to even, in [-7, 7], stored as k + 8
+// in 4 bits. k has at most 3 significant bits and s has 5, so the value k s has
+// at most 8: it is exact in bf16, and every kernel multiplies the same numbers
+// whether it works in bf16 or in fp32. The rounding to k is the only loss.
+// 4 + 16/32 = 4.5 bits an element.
+//
+// Layout (one buffer): codes [L][K|V][B][H][Pp][Dh/2] bytes (dim 2i in the low
+// half of byte i), then scales [L][K|V][B][H][Pp][Dh/32] bf16; Pp = P rounded up
+// to the 128-key tile. Head-major, so that the rows an attention CTA reads are
+// contiguous; every row carries its own scales, so that evicting rows is a plain
+// gather. Rows [P, Pp) are never written, and no kernel lets what they (or the
+// rows behind an item's own length) hold reach a result.
+#pragma once
+#include "qi21_common.cuh"
+
+namespace qi21 {
+
+constexpr int KV4_GROUP = 32;
+
+struct Kv4Dims {
+    int B, H, P, Pp, Dh;
+    int64_t scales_off;          // bytes from the buffer's start to the scales
+};
+
+__host__ __device__ __forceinline__ int64_t kv4_pad(int64_t P) { return (P + 127) / 128 * 128; }
+
+// First row of (layer l, which = 0 K / 1 V, item b, head h), in rows.
+__host__ __device__ __forceinline__ int64_t kv4_row0(const Kv4Dims &c, int l, int which, int b, int h) {
+    return ((((int64_t)l * 2 + which) * c.B + b) * c.H + h) * c.Pp;
+}
+
+// Rows of item b that exist: its own length where the cache has lengths, else P.
+__device__ __forceinline__ int kv4_len(const Kv4Dims &c, const int *prefix_len, int b) {
+    if (!prefix_len) return c.P;
+    const int n = prefix_len[b];
+    return n < 0 ? 0 : (n > c.P ? c.P : n);
+}
+
+// ------------------------------------------------------------------ quantise
+// 8 consecutive elements of a row as floats.
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const bf16 *p, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(bf16 *p, const float (&x)[8]) {   // exact: every value has 8 bits
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The scale of a group whose largest magnitude has these bits (finite or not).
+// The candidate cuts a/7 (a product with the rounded 1/7, within 2^-23 of it) to
+// 5 bits; one step up where 7 times it falls short. 7 * (5 bits) is exact in
+// fp32, so the test is exact. A NaN or an infinity anywhere makes the scale NaN.
+__device__ __forceinline__ float kv4_scale(uint32_t amax_bits) {
+    if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    const float a = __uint_as_float(amax_bits);
+    if (a == 0.f) return 0.f;
+    constexpr float lo = 1.17549435e-38f, hi = 5.316911983e36f;   // 2^-126, 2^122
+    float s = __uint_as_float(__float_as_uint(a * 0.142857149f) & 0xFFF80000u);
+    if (s < lo) s = lo;      // below the smallest normal number there are not 5 bits
+    if (7.f * s < a) s = __uint_as_float(__float_as_uint(s) + 0x00080000u);
+    return fminf(s, hi);
+}
+
+// rint(x / s) in [-7, 7], ties to even, for s > 0 with r = fl(1 / s). t = x r is
+// within 2^-22 |t| of the quotient: where it lies near the middle of two integers
+// the exact remainder x - k s decides (k s has 8 bits, and the difference is
+// exact there: Sterbenz, or k = 0).
+__device__ __forceinline__ float kv4_code(float x, float s, float r) {
+    const float t = fminf(fmaxf(x * r, -7.f), 7.f);
+    float k = rintf(t);
+    if (fabsf(t - k) > 0.4999f) {
+        const float e = fmaf(-k, s, x), e2 = 2.f * fabsf(e);
+        if (e2 > s || (e2 == s && ((int)k & 1))) k += copysignf(1.f, e);
+        k = fminf(fmaxf(k, -7.f), 7.f);
+    }
+    return k;
+}
+
+constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row kernels handles
+
+// Quantise rows [0, P) of every (layer, K|V, item) slab of a cache in token-major
+// layout (slab stride in elements) into the 4-bit layout. A thread takes 8
+// consecutive dims of 4 consecutive rows (16 bytes a row in bf16; the four scales
+// of a row quad and column share a 32-byte sector at head_dim 128), the four
+// threads of a group share its maximum by two shuffles. Bound by HBM: eb + 0.5625
+// bytes an element.
+template <typename T>
+__global__ void __launch_bounds__(256) k_kv4_quantize(const T *__restrict__ src, int64_t slab_stride, Kv4Dims c,
+                                                      const int *__restrict__ prefix_len, uint8_t *__restrict__ base) {
+    const int d = c.H * c.Dh, cols = d / 8;
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int slab = blockIdx.y;                 // (l * 2 + which) * B + b
+    const int rows = kv4_len(c, prefix_len, slab % c.B);
+    const int64_t quad = u / cols;
+    const int col = (int)(u - quad * cols);      // the 4 threads of a group are lanes of one warp: cols % 4 == 0
+    const int h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
+    float x[KV4_Q_ROWS][8];
+#pragma unroll
+    for (int i = 0; i < KV4_Q_ROWS; ++i) {
+        const int64_t r = quad * KV4_Q_ROWS + i;
+        if (r < rows) {
+            load8(src + slab * slab_stride + r * d + col * 8, x[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
+        }
+    }
+    const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp;
+#pragma unroll
+    for (int i = 0; i < KV4_Q_ROWS; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[i][k]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const float s = kv4_scale(m), r = s > 0.f ? 1.f / s : 0.f;
+        uint32_t w = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float q = s > 0.f ? kv4_code(x[i][k], s, r) : 0.f;
+            w |= (uint32_t)((int)q + 8) << (4 * k);
+        }
+        const int64_t row = quad * KV4_Q_ROWS + i;
+        if (row < rows) {
+            *reinterpret_cast<uint32_t *>(base + (row0 + row) * (c.Dh / 2) + j0 / 2) = w;
+            if ((col & 3) == 0)
+                reinterpret_cast<uint16_t *>(base + c.scales_off)[(row0 + row) * (c.Dh / KV4_GROUP) + j0 / KV4_GROUP] =
+                    (uint16_t)(__float_as_uint(s) >> 16);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dequantise
+// The 8 values of a code word.
+__device__ __forceinline__ void kv4_values(uint32_t w, float s, float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = (float)((int)((w >> (4 * k)) & 15u) - 8) * s;
+}
+__device__ __forceinline__ float kv4_load_scale(const uint8_t *base, const Kv4Dims &c, int64_t row, int group) {
+    return __uint_as_float(
+        (uint32_t)reinterpret_cast<const uint16_t *>(base + c.scales_off)[row * (c.Dh / KV4_GROUP) + group] << 16);
+}
+
+// The way back: rows [0, len) of every slab in token-major layout, the mapping of
+// k_kv4_quantize.
+template <typename T>
+__global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *__restrict__ base, Kv4Dims c,
+                                                        const int *__restrict__ prefix_len, T *__restrict__ dst,
+                                                        int64_t slab_stride) {
+    const int d = c.H * c.Dh, cols = d / 8;
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int slab = blockIdx.y;
+    const int rows = kv4_len(c, prefix_len, slab % c.B);
+    const int64_t quad = u / cols;
+    const int col = (int)(u - quad * cols);
+    const int h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
+    const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp;
+    uint32_t w[KV4_Q_ROWS];
+    float s[KV4_Q_ROWS];
+#pragma unroll
+    for (int i = 0; i < KV4_Q_ROWS; ++i) {
+        const int64_t r = quad * KV4_Q_ROWS + i;
+        if (r < rows) {
+            w[i] = *reinterpret_cast<const uint32_t *>(base + (row0 + r) * (c.Dh / 2) + j0 / 2);
+            s[i] = kv4_load_scale(base, c, row0 + r, j0 / KV4_GROUP);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < KV4_Q_ROWS; ++i) {
+        const int64_t r = quad * KV4_Q_ROWS + i;
+        if (r < rows) {
+            float x[8];
+            kv4_values(w[i], s[i], x);
+            store8(dst + slab * slab_stride + r * d + col * 8, x);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ eviction
+// Order of the eviction: protected rows first, then by score; a NaN score counts
+// as the lowest of all.
+__device__ __forceinline__ uint32_t kv4_rank(float s, int j, int n_protected) {
+    if (j < n_protected) return 0xFFFFFFFFu;
+    if (s != s) return 0u;
+    const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);       // -0 ranks as +0
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+constexpr int KV4_SEL_THREADS = 512;
+
+// Exclusive prefix sum of a flag over the block (all threads call); *total on every thread.
+__device__ __forceinline__ int kv4_block_rank(bool f, int *warp_sums, int *total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const uint32_t m = __ballot_sync(0xffffffffu, f);
+    __syncthreads();
+    if (lane == 0) warp_sums[wid] = __popc(m);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < KV4_SEL_THREADS / 32; ++i) {
+        const int n = warp_sums[i];
+        if (i < wid) before += n;
+        all += n;
+    }
+    *total = all;
+    return before + __popc(m & ((1u << lane) - 1));
+}
+
+// The rows that one (layer, item, head) keeps: the `keep` largest of its ranks,
+// ties to the lowest row, in ascending order; -1 behind them where the item has
+// fewer rows. Radix selection, 8 bits a pass from the top, on integers: exact, and
+// the same whatever the order of the atomics. grid (H, B, L).
+__global__ void __launch_bounds__(KV4_SEL_THREADS)
+    k_kv4_select(const float *__restrict__ scores, Kv4Dims c, const int *__restrict__ prefix_len, int keep,
+                 int n_protected, int *__restrict__ kept, int *__restrict__ dst_len) {
+    __shared__ int hist[256];
+    __shared__ int warp_sums[KV4_SEL_THREADS / 32];
+    __shared__ int sel[2];
+    const int h = blockIdx.x, b = blockIdx.y, l = blockIdx.z;
+    const int64_t lbh = ((int64_t)l * c.B + b) * c.H + h;
+    const float *sc = scores + lbh * c.P;
+    int *out = kept + lbh * keep;
+    const int len = kv4_len(c, prefix_len, b);
+    const int count = min(keep, len);
+    if (dst_len && l == 0 && h == 0 && threadIdx.x == 0) dst_len[b] = count;
+    uint32_t prefix = 0;         // the bits of the count-th largest rank found so far
+    int need = count;            // how many ranks with these bits are taken
+    if (count < len) {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < 256; i += KV4_SEL_THREADS) hist[i] = 0;
+            __syncthreads();
+            const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+            for (int j = threadIdx.x; j < len; j += KV4_SEL_THREADS) {
+                const uint32_t r = kv4_rank(sc[j], j, n_protected);
+                if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & 255], 1);
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                int n = need, d = 255;
+                while (d > 0 && hist[d] < n) n -= hist[d--];
+                sel[0] = d;
+                sel[1] = n;
+            }
+            __syncthreads();
+            prefix |= (uint32_t)sel[0] << shift;
+            need = sel[1];
+        }
+    }
+    int ties = 0, taken = 0;
+    for (int j0 = 0; j0 < len; j0 += KV4_SEL_THREADS) {
+        const int j = j0 + threadIdx.x;
+        const uint32_t r = j < len ? kv4_rank(sc[j], j, n_protected) : 0u;
+        int n;
+        bool take = j < len;
+        if (count < len) {
+            const bool tie = j < len && r == prefix;
+            const int before = ties + kv4_block_rank(tie, warp_sums, &n);
+            ties += n;
+            take = j < len && (r > prefix || (tie && before < need));
+        }
+        const int at = taken + kv4_block_rank(take, warp_sums, &n);
+        taken += n;
+        if (take && at < count) out[at] = j;
+    }
+    for (int i = count + threadIdx.x; i < keep; i += KV4_SEL_THREADS) out[i] = -1;
+}
+
+// Copy the kept rows of K and V into the smaller cache. A thread moves one group
+// (16 bytes of codes and its scale) of a row of K and of V. grid (pieces, H, L * B).
+__global__ void __launch_bounds__(256)
+    k_kv4_gather(const uint8_t *__restrict__ src, Kv4Dims c, const int *__restrict__ kept, int keep,
+                 uint8_t *__restrict__ dst, Kv4Dims o) {
+    const int G = c.Dh / KV4_GROUP;
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int r = (int)(u / G), g = (int)(u - (int64_t)r * G);
+    if (r >= keep) return;
+    const int h = blockIdx.y, l = blockIdx.z / c.B, b = blockIdx.z - l * c.B;
+    const int j = kept[(((int64_t)l * c.B + b) * c.H + h) * keep + r];
+    if (j < 0) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const int64_t from = (kv4_row0(c, l, which, b, h) + j) * G + g, to = (kv4_row0(o, l, which, b, h) + r) * G + g;
+        reinterpret_cast<uint4 *>(dst)[to] = reinterpret_cast<const uint4 *>(src)[from];
+        reinterpret_cast<uint16_t *>(dst + o.scales_off)[to] =
+            reinterpret_cast<const uint16_t *>(src + c.scales_off)[from];
+    }
+}
+
+// ------------------------------------------------------------------ CUDA-core attention
+// Keys of an item, in this order: its prefix rows [0, len) from the 4-bit cache,
+// then its n_tail tail rows (token-major, storage dtype). 32 query rows x 32 keys
+// a step, 128 threads: 2 x 4 scores a thread, then 4 rows x DH/16 dims of the
+// output. fp32 throughout. The keys are split over n_split CTAs whose normalised
+// partial outputs and log2-sum-exps k_kv4_combine joins.
+struct Kv4AttnArgs {
+    const uint8_t *base;
+    Kv4Dims c;
+    const int *prefix_len;
+    int layer;
+    int shared;                  // 1: every item reads cache item 0
+    const void *q;               // [B][n_q][d]
+    int B, n_q;
+    const void *k_tail, *v_tail; // [B][n_tail][d]
+    int n_tail;
+    void *out;                   // [B][n_q][d]
+    float *lse;                  // [H][B][n_q] or null
+    int n_split;
+    float *part_l;               // [B][H][n_split][n_q]       log2-sum-exp
+    float *part_o;               // [B][H][n_split][n_q][DH]
+    float scale_log2;            // log2(e) / sqrt(Dh)
+    uint32_t *err;
+};
+
+constexpr float KV4_LN2 = 0.69314718055994531f;
+
+// Rows [r0, r0 + 32) of one head of a token-major tensor into shared memory, zeros behind n.
+template <typename T, int DH>
+__device__ __forceinline__ void kv4_stage_rows(float *dst, const T *src, int r0, int n, int d) {
+    for (int e = threadIdx.x; e < 32 * (DH / 8); e += 128) {
+        const int i = e / (DH / 8), c8 = e - i * (DH / 8);
+        float x[8];
+        if (r0 + i < n) {
+            load8(src + (int64_t)(r0 + i) * d + c8 * 8, x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = 0.f;
+        }
+        store8(dst + i * (DH + 4) + c8 * 8, x);
+    }
+}
+
+// Keys [k0, k0 + 32) of an item (prefix, then tail), zeros from k_end on.
+template <typename T, int DH>
+__device__ __forceinline__ void kv4_stage_keys(float *dst, const uint8_t *base, const Kv4Dims &c, int64_t row0,
+                                               int len, const T *tail, int d, int k0, int k_end) {
+    for (int e = threadIdx.x; e < 32 * (DH / 8); e += 128) {
+        const int i = e / (DH / 8), c8 = e - i * (DH / 8), key = k0 + i;
+        float x[8];
+        if (key < k_end && key < len) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(base + (row0 + key) * (DH / 2) + c8 * 4);
+            kv4_values(w, kv4_load_scale(base, c, row0 + key, c8 / 4), x);
+        } else if (key < k_end) {
+            load8(tail + (int64_t)(key - len) * d + c8 * 8, x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = 0.f;
+        }
+        store8(dst + i * (DH + 4) + c8 * 8, x);
+    }
+}
+
+// acc[i][j] = A[2 ty + i] . B[tx + 8 j] over DH, both [32][DH + 4] in shared memory.
+template <int DH>
+__device__ __forceinline__ void kv4_tile_product(const float *A, const float *Bm, int ty, int tx, float (&acc)[2][4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < DH; k += 4) {
+        float4 a[2], b[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (2 * ty + i) * (DH + 4) + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(Bm + (tx + 8 * j) * (DH + 4) + k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+            }
+    }
+}
+
+template <int DH>
+constexpr size_t kv4_attn_simt_smem() {
+    return sizeof(float) * (3 * 32 * (DH + 4) + 32 * 36 + 3 * 32);
+}
+
+// grid (query tiles, H, B * n_split)
+template <typename T, int DH>
+__global__ void __launch_bounds__(128) k_kv4_attn_simt(Kv4AttnArgs p) {
+    extern __shared__ __align__(16) float sm4[];
+    float *Qs = sm4, *Ks = Qs + 32 * (DH + 4), *Vs = Ks + 32 * (DH + 4);
+    float *Ps = Vs + 32 * (DH + 4);          // [key][36]: row r of key k at k * 36 + r
+    float *al = Ps + 32 * 36, *ls = al + 32, *ms = ls + 32;
+    const int h = blockIdx.y, b = blockIdx.z / p.n_split, sp = blockIdx.z - b * p.n_split;
+    const int q0 = blockIdx.x * 32, d = p.c.H * DH, cb = p.shared ? 0 : b;
+    const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7, py = tid >> 4, px = tid & 15;
+    const int len = kv4_len(p.c, p.prefix_len, cb), keys = len + p.n_tail;
+    const int per = ((keys + p.n_split - 1) / p.n_split + 31) / 32 * 32;
+    const int k_lo = min(keys, sp * per), k_hi = min(keys, k_lo + per);
+    const int64_t k_row0 = kv4_row0(p.c, p.layer, 0, cb, h), v_row0 = kv4_row0(p.c, p.layer, 1, cb, h);
+    const T *kt = (const T *)p.k_tail + (int64_t)b * p.n_tail * d + h * DH;
+    const T *vt = (const T *)p.v_tail + (int64_t)b * p.n_tail * d + h * DH;
+    kv4_stage_rows<T, DH>(Qs, (const T *)p.q + (int64_t)b * p.n_q * d + h * DH, q0, p.n_q, d);
+    constexpr int NC = DH / 16;
+    float o[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) o[i][j] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int k0 = k_lo; k0 < k_hi; k0 += 32) {
+        __syncthreads();
+        kv4_stage_keys<T, DH>(Ks, p.base, p.c, k_row0, len, kt, d, k0, k_hi);
+        kv4_stage_keys<T, DH>(Vs, p.base, p.c, v_row0, len, vt, d, k0, k_hi);
+        __syncthreads();
+        float s[2][4];
+        kv4_tile_product<DH>(Qs, Ks, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = k0 + tx + 8 * j < k_hi ? s[i][j] * p.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float mn = fmaxf(m[i], mx), mz = mn == -INFINITY ? 0.f : mn;
+            const float a = exp2f(m[i] - mz);      // the tile has a key, so mn is finite unless a score is -inf
+            float rs = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e = exp2f(s[i][j] - mz);
+                Ps[(tx + 8 * j) * 36 + 2 * ty + i] = e;
+                rs += e;
+            }
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, x);
+            l[i] = l[i] * a + rs;
+            m[i] = mn;
+            if (tx == 0) al[2 * ty + i] = a;
+        }
+        __syncthreads();
+        float av[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = al[4 * py + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) o[i][j] *= av[i];
+#pragma unroll 4
+        for (int k = 0; k < 32; ++k) {
+            const float4 pr = *reinterpret_cast<const float4 *>(Ps + k * 36 + 4 * py);
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const float v = Vs[k * (DH + 4) + px + 16 * j];
+                o[0][j] = fmaf(pr.x, v, o[0][j]);
+                o[1][j] = fmaf(pr.y, v, o[1][j]);
+                o[2][j] = fmaf(pr.z, v, o[2][j]);
+                o[3][j] = fmaf(pr.w, v, o[3][j]);
+            }
+        }
+    }
+    __syncthreads();
+    if (tx == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            ls[2 * ty + i] = l[i];
+            ms[2 * ty + i] = m[i];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * py + i, row = q0 + r;
+        if (row >= p.n_q) continue;
+        const float lr = ls[r], inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);   // no key: 0; NaN stays
+        const float lse2 = lr > 0.f ? ms[r] + log2f(lr) : (lr == 0.f ? -INFINITY : lr);
+        if (p.n_split == 1) {
+            T *dst = (T *)p.out + ((int64_t)b * p.n_q + row) * d + h * DH;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) dst[px + 16 * j] = from_f<T>(o[i][j] * inv);
+            if (p.lse && px == 0) p.lse[((int64_t)h * p.B + b) * p.n_q + row] = lse2 * KV4_LN2;
+        } else {
+            const int64_t at = (((int64_t)b * p.c.H + h) * p.n_split + sp) * p.n_q + row;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) p.part_o[at * DH + px + 16 * j] = o[i][j] * inv;
+            if (px == 0) p.part_l[at] = lse2;
+        }
+    }
+}
+
+// Join the partial results of the key splits: with w_s = 2^(lse_s - max),
+// out = sum w_s o_s / sum w_s, lse = max + log2 sum w_s; rows without any key get
+// 0 and -inf. A warp per (item, head, row), in a fixed order. grid (rows / 8, H, B).
+template <typename T, int DH>
+__global__ void __launch_bounds__(256) k_kv4_combine(Kv4AttnArgs p) {
+    const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
+    if (row >= p.n_q) return;
+    const int64_t at0 = ((int64_t)b * p.c.H + h) * p.n_split * p.n_q + row;
+    float m = -INFINITY;
+    for (int s = 0; s < p.n_split; ++s) m = fmaxf(m, p.part_l[at0 + (int64_t)s * p.n_q]);
+    const float mz = m == -INFINITY ? 0.f : m;
+    float sum = 0.f, o[DH / 32];
+#pragma unroll
+    for (int j = 0; j < DH / 32; ++j) o[j] = 0.f;
+    for (int s = 0; s < p.n_split; ++s) {
+        const int64_t at = at0 + (int64_t)s * p.n_q;
+        const float w = exp2f(p.part_l[at] - mz);
+        sum += w;
+#pragma unroll
+        for (int j = 0; j < DH / 32; ++j) o[j] = fmaf(w, p.part_o[at * DH + lane + 32 * j], o[j]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int d = p.c.H * DH;
+    T *dst = (T *)p.out + ((int64_t)b * p.n_q + row) * d + h * DH;
+#pragma unroll
+    for (int j = 0; j < DH / 32; ++j) dst[lane + 32 * j] = from_f<T>(o[j] * inv);
+    if (p.lse && lane == 0)
+        p.lse[((int64_t)h * p.B + b) * p.n_q + row] = sum == 0.f ? -INFINITY : (mz + log2f(sum)) * KV4_LN2;
+}
+
+// ------------------------------------------------------------------ CUDA-core scores
+// out[b][h][j] = in[b][h][j] + sum_i exp(q_i . k_j / sqrt(Dh) - lse_i) for the rows
+// j < len of cache item b, over the queries i of every item that reads it. 32 keys
+// a CTA, every query in steps of 32; the sum over queries is the CTA's own, in a
+// fixed order. grid (key tiles, H, cache items).
+struct Kv4ScoreArgs {
+    const uint8_t *base;
+    Kv4Dims c;
+    const int *prefix_len;
+    int layer;
+    const void *q;               // [cache items][n_q][d]
+    int n_q;                     // query rows per cache item
+    const float *lse;            // [H][cache items * n_q], natural log
+    const float *in;             // [B][H][P] or null (zeros)
+    float *out;                  // may be in
+    float scale_log2;
+    uint32_t *err;
+};
+
+template <int DH>
+constexpr size_t kv4_scores_simt_smem() {
+    return sizeof(float) * (2 * 32 * (DH + 4) + 32);
+}
+
+// The exponent's offset of a query row: log2 of its sum, +inf (weight 0) for a row
+// that had no key.
+__device__ __forceinline__ float kv4_lse2(float lse) {
+    return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(128) k_kv4_scores_simt(Kv4ScoreArgs p) {
+    extern __shared__ __align__(16) float sm4[];
+    float *Ks = sm4, *Qs = Ks + 32 * (DH + 4), *lq = Qs + 32 * (DH + 4);
+    const int h = blockIdx.y, b = blockIdx.z, k0 = blockIdx.x * 32, d = p.c.H * DH;
+    const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7;
+    const int len = kv4_len(p.c, p.prefix_len, b);
+    if (p.out != p.in) {
+        for (int i = tid; i < 32; i += 128) {           // rows behind the item's own keep what they had
+            const int j = k0 + i;
+            const int64_t at = ((int64_t)b * p.c.H + h) * p.c.P + j;
+            if (j >= len && j < p.c.P) p.out[at] = p.in ? p.in[at] : 0.f;
+        }
+    }
+    if (k0 >= len) return;
+    kv4_stage_keys<T, DH>(Ks, p.base, p.c, kv4_row0(p.c, p.layer, 0, b, h), len, nullptr, d, k0, len);
+    const T *q = (const T *)p.q + (int64_t)b * p.n_q * d + h * DH;
+    const float *lse = p.lse + ((int64_t)h * p.c.B + b) * p.n_q;
+    float sum[2] = {0.f, 0.f};
+    for (int q0 = 0; q0 < p.n_q; q0 += 32) {
+        __syncthreads();
+        kv4_stage_rows<T, DH>(Qs, q, q0, p.n_q, d);
+        if (tid < 32) lq[tid] = q0 + tid < p.n_q ? kv4_lse2(lse[q0 + tid]) : INFINITY;
+        __syncthreads();
+        float s[2][4];
+        kv4_tile_product<DH>(Ks, Qs, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[i] += exp2f(s[i][j] * p.scale_log2 - lq[tx + 8 * j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float t = sum[i];
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+        const int j = k0 + 2 * ty + i;
+        if (tx == 0 && j < len) {
+            const int64_t at = ((int64_t)b * p.c.H + h) * p.c.P + j;
+            p.out[at] = (p.in ? p.in[at] : 0.f) + t;
+        }
+    }
+}
+
+}  // namespace qi21

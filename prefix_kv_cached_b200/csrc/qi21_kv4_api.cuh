@@ -1,0 +1,160 @@
+// Launches of the 4-bit prefix cache's operators and their argument checks
+// (included by qi21_api.cu; the kernels are in qi21_kv4.cuh).
+#pragma once
+#include "qi21_kv4.cuh"
+
+namespace qi21 {
+
+static Kv4Dims kv4_dims(const qi21_kv4_cache &k) {
+    Kv4Dims c{};
+    c.B = k.batch;
+    c.H = k.n_heads;
+    c.P = k.n_prefix;
+    c.Pp = (int)kv4_pad(k.n_prefix);
+    c.Dh = k.head_dim;
+    c.scales_off = (int64_t)k.n_layers * 2 * c.B * c.H * c.Pp * (c.Dh / 2);
+    return c;
+}
+
+// A cache descriptor against the config: sizes that match and fit the launches.
+static qi21_status check_kv4(const qi21_config *c, const qi21_kv4_cache *k) {
+    if (!k || !al16(k->base) || ((uintptr_t)k->prefix_len & 15)) return QI21_ERR_INVALID_ARG;
+    if (!kv4_head_dim_ok(*c)) return QI21_ERR_UNSUPPORTED;
+    if (k->n_layers != c->n_layers || k->n_heads != c->n_heads || k->head_dim != c->head_dim || k->batch <= 0 ||
+        k->n_prefix <= 0 || k->n_prefix > INT32_MAX - 128)
+        return QI21_ERR_CACHE_STATE;
+    if ((int64_t)k->n_layers * 2 * k->batch > 65535 || k->n_heads > 65535) return QI21_ERR_SHAPE;
+    return QI21_OK;
+}
+
+// A token-major cache and a 4-bit one that hold the same prefix rows.
+static bool kv4_matches(const qi21_config *c, const qi21_kv_cache *a, const qi21_kv4_cache *k) {
+    return a->n_layers == c->n_layers && a->d_model == c->d_model && a->dtype == c->dtype && a->batch > 0 &&
+           a->n_target > 0 && a->n_prefix == k->n_prefix && k->batch == (a->shared_prefix ? 1 : a->batch);
+}
+
+static int64_t kv_slab_rows(const qi21_kv_cache &a) {
+    return a.shared_prefix ? kv4_pad(a.n_prefix) + (int64_t)a.batch * a.n_target
+                           : (int64_t)a.n_prefix + a.n_target;
+}
+
+static dim3 kv4_row_grid(const qi21_config &c, const qi21_kv4_cache &k) {
+    const int64_t units = ((int64_t)k.n_prefix + KV4_Q_ROWS - 1) / KV4_Q_ROWS * (c.d_model / 8);
+    return dim3((unsigned)((units + 255) / 256), (unsigned)(c.n_layers * 2 * k.batch));
+}
+
+template <typename T>
+static void launch_kv4_quantize(Launcher &L, const qi21_config &c, const qi21_kv_cache &src,
+                                const qi21_kv4_cache &dst) {
+    L.run("kv4_quantize", [&] {
+        k_kv4_quantize<T><<<kv4_row_grid(c, dst), 256, 0, L.st>>>((const T *)src.base, kv_slab_rows(src) * c.d_model,
+                                                                  kv4_dims(dst), dst.prefix_len, (uint8_t *)dst.base);
+    });
+}
+
+template <typename T>
+static void launch_kv4_dequantize(Launcher &L, const qi21_config &c, const qi21_kv4_cache &src,
+                                  const qi21_kv_cache &dst) {
+    L.run("kv4_dequantize", [&] {
+        k_kv4_dequantize<T><<<kv4_row_grid(c, src), 256, 0, L.st>>>((const uint8_t *)src.base, kv4_dims(src),
+                                                                    src.prefix_len, (T *)dst.base,
+                                                                    kv_slab_rows(dst) * c.d_model);
+    });
+}
+
+template <typename T, int DH>
+static void launch_kv4_attn_simt(Launcher &L, const Kv4AttnArgs &p) {
+    constexpr size_t smem = kv4_attn_simt_smem<DH>();
+    static DeviceFlags attr;
+    smem_opt_in(k_kv4_attn_simt<T, DH>, (int)smem, attr);
+    L.run("kv4_attn_simt", [&] {
+        k_kv4_attn_simt<T, DH><<<dim3((p.n_q + 31) / 32, p.c.H, p.B * p.n_split), 128, smem, L.st>>>(p);
+    });
+    if (p.n_split > 1)
+        L.run("kv4_combine", [&] {
+            k_kv4_combine<T, DH><<<dim3((p.n_q + 7) / 8, p.c.H, p.B), 256, 0, L.st>>>(p);
+        });
+}
+
+// Attention of one layer; ws: the region that kv4_plan() lays out.
+template <typename T>
+static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_kv4_cache &k, int layer, const void *q,
+                                 int B, int n_q, const void *k_tail, const void *v_tail, int n_tail, void *out,
+                                 float *lse, char *ws, uint32_t *err) {
+    const Kv4Plan plan = kv4_plan(c, B, n_q, k.n_prefix, n_tail);
+    Kv4AttnArgs p{};
+    p.base = (const uint8_t *)k.base;
+    p.c = kv4_dims(k);
+    p.prefix_len = k.prefix_len;
+    p.layer = layer;
+    p.shared = k.batch == 1;
+    p.q = q;
+    p.B = B;
+    p.n_q = n_q;
+    p.k_tail = k_tail;
+    p.v_tail = v_tail;
+    p.n_tail = n_tail;
+    p.out = out;
+    p.lse = lse;
+    p.n_split = plan.n_split;
+    p.part_l = (float *)(ws + plan.part_l);
+    p.part_o = (float *)(ws + plan.part_o);
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
+    p.err = err;
+    switch (c.head_dim) {
+        case 32: launch_kv4_attn_simt<T, 32>(L, p); break;
+        case 64: launch_kv4_attn_simt<T, 64>(L, p); break;
+        case 96: launch_kv4_attn_simt<T, 96>(L, p); break;
+        default: launch_kv4_attn_simt<T, 128>(L, p); break;
+    }
+}
+
+template <typename T, int DH>
+static void launch_kv4_scores_simt(Launcher &L, const Kv4ScoreArgs &p) {
+    constexpr size_t smem = kv4_scores_simt_smem<DH>();
+    static DeviceFlags attr;
+    smem_opt_in(k_kv4_scores_simt<T, DH>, (int)smem, attr);
+    L.run("kv4_scores_simt", [&] {
+        k_kv4_scores_simt<T, DH><<<dim3((p.c.P + 31) / 32, p.c.H, p.c.B), 128, smem, L.st>>>(p);
+    });
+}
+
+template <typename T>
+static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_cache &k, int layer, const void *q,
+                              int B, int n_q, const float *lse, const float *in, float *out, char *ws,
+                              uint32_t *err) {
+    Kv4ScoreArgs p{};
+    p.base = (const uint8_t *)k.base;
+    p.c = kv4_dims(k);
+    p.prefix_len = k.prefix_len;
+    p.layer = layer;
+    p.q = q;
+    p.n_q = k.batch == 1 ? B * n_q : n_q;      // one item: the rows of every request that reads it
+    p.lse = lse;
+    p.in = in;
+    p.out = out;
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
+    p.err = err;
+    switch (c.head_dim) {
+        case 32: launch_kv4_scores_simt<T, 32>(L, p); break;
+        case 64: launch_kv4_scores_simt<T, 64>(L, p); break;
+        case 96: launch_kv4_scores_simt<T, 96>(L, p); break;
+        default: launch_kv4_scores_simt<T, 128>(L, p); break;
+    }
+}
+
+// Shared checks of the attention, the scores and the cached step.
+static qi21_status check_kv4_queries(const qi21_config *c, const qi21_kv4_cache *k, int32_t B, int32_t n_q,
+                                     int32_t n_tail) {
+    qi21_status s = check_kv4(c, k);
+    if (s) return s;
+    if (k->state != QI21_CACHE_EXTRACTED) return QI21_ERR_CACHE_STATE;
+    if (B <= 0 || n_q <= 0 || n_tail < 0) return QI21_ERR_SHAPE;
+    if (k->batch != B && k->batch != 1) return QI21_ERR_CACHE_STATE;
+    // one 32-bit index holds every query row, and every key of an item
+    if ((int64_t)B * n_q > INT32_MAX - 256 || (int64_t)k->n_prefix + n_tail > INT32_MAX - 256) return QI21_ERR_SHAPE;
+    if ((int64_t)B * kv4_plan(*c, B, n_q, k->n_prefix, n_tail).n_split > 65535) return QI21_ERR_SHAPE;
+    return QI21_OK;
+}
+
+}  // namespace qi21

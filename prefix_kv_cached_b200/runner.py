@@ -134,6 +134,67 @@ class Qi21Runner:
     def euler(self, x: torch.Tensor, v: torch.Tensor, s0: float, s1: float, x_out: torch.Tensor):
         B.check("qi21_euler_update", B.qi21_euler_update(x, v, s0, s1, x_out, x.numel(), self.stream))
 
+    # ------------------------------------------------------------------ 4-bit prefix cache
+
+    def quantise_prefix(self):
+        """Hold the extracted prefix in 4 bits from here on (for cached_step_kv4);
+        the cache buffer itself is kept for the next extract."""
+        nb = 1 if self.shared_prefix else self.Bn
+        self.kv4_buf = torch.empty(B.qi21_kv4_cache_bytes(self.cfg, nb, self.P), dtype=torch.uint8,
+                                   device=self.device)
+        self.kv4 = B.qi21_kv4_cache_init(self.kv4_buf, self.cfg, nb, self.P)
+        B.check("qi21_kv4_quantize", B.qi21_kv4_quantize(self.cfg, self.cache, self.kv4, self.stream))
+        self.kv4_scores: Optional[torch.Tensor] = None
+        # the whole prefix needs the largest workspace
+        self.kv4_ws = torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, self.P, self.N),
+                                  dtype=torch.uint8, device=self.device)
+
+    def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
+        """The cached step over the 4-bit prefix. accumulate: add every layer's
+        attention weights of this step to kv4_scores [L][items][H][rows]."""
+        if accumulate and self.kv4_scores is None:
+            k = self.kv4
+            self.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix, dtype=torch.float32,
+                                          device=self.device)
+        B.check("qi21_cached_step_kv4", B.qi21_cached_step_kv4(
+            self.cfg, self.wstruct, self.kv4, self.Bn, self.N, x, self.cos_sin_target, self.mod_target,
+            self.scale_final, v_out, self.kv4_scores if accumulate else None, self.kv4_ws, self.kv4_ws.numel(),
+            self.stream))
+
+    def evict_prefix(self, keep: int, n_protected: int = 0) -> torch.Tensor:
+        """Shrink the 4-bit prefix to the `keep` rows of every head that the steps
+        with accumulate=True attended to most (the first n_protected rows stay in
+        any case). Returns the rows kept, int32 [L][items][H][keep]; the weights
+        start again at zero."""
+        if self.kv4_scores is None:
+            raise ValueError("evict_prefix needs a cached_step_kv4 with accumulate=True before it")
+        k = self.kv4
+        buf = torch.empty(B.qi21_kv4_cache_bytes(self.cfg, k.batch, keep), dtype=torch.uint8, device=self.device)
+        small = B.qi21_kv4_cache_init(buf, self.cfg, k.batch, keep)
+        kept = torch.empty(k.n_layers, k.batch, k.n_heads, keep, dtype=torch.int32, device=self.device)
+        B.check("qi21_kv4_evict", B.qi21_kv4_evict(self.cfg, k, self.kv4_scores, keep, n_protected, small, kept,
+                                                   self.stream))
+        self.kv4, self.kv4_buf, self.kv4_scores = small, buf, None
+        return kept
+
+    def denoise_kv4(self, prefix_hidden: torch.Tensor, x0: torch.Tensor, sigmas=None, keep: Optional[int] = None,
+                    n_protected: int = 0):
+        """denoise() with the prefix held in 4 bits; keep: after the first step, go
+        on with the `keep` prefix rows of every head that it attended to most."""
+        sigmas = self.w.sigmas if sigmas is None else sigmas
+        self.set_prefix_row()
+        self.prefix_extract(prefix_hidden)
+        self.quantise_prefix()
+        x = x0.clone()
+        v = torch.empty_like(x)
+        for k in range(len(sigmas) - 1):
+            self.set_target_row(sigmas[k])
+            self.cached_step_kv4(x, v, accumulate=keep is not None and k == 0)
+            if keep is not None and k == 0:
+                self.evict_prefix(keep, n_protected)
+            self.euler(x, v, sigmas[k], sigmas[k + 1], x)
+        return x
+
     # ------------------------------------------------------------------ whole image
 
     def denoise_image(self, prefix_hidden: torch.Tensor, x: torch.Tensor, sigmas_dev: torch.Tensor,
