@@ -95,23 +95,61 @@ inline WsLayout ws_layout(const qi21_config &c, int64_t B, int64_t P, int64_t N)
     return L;
 }
 
-// Plan of an attention over a 4-bit cache: how the keys are split, and the fp32
-// partial results (log2-sum-exp, then normalised outputs) in the workspace. Host
-// arithmetic on sizes alone, so that the size query and the call agree.
+// Plan of an attention over a 4-bit cache: which kernel, how the work is cut, and
+// the fp32 partial results (log2-sum-exp, then normalised outputs) in the
+// workspace. Host arithmetic on sizes alone, so that the size query and the call
+// agree; 148 is the number of SMs the cuts are made for, not one they need.
+//   Kv4Work: the tensor-core kernel's steps. A step is one 128-key tile of one unit
+//   (item, head, unit_rows query rows); `units` units of `tiles` steps each, laid
+//   end to end, are shared out over `grid` CTAs: evenly, or (whole = 1) in whole
+//   units. slot_rows: rows of a partial-result slot, two slots a CTA.
+struct Kv4Work {
+    int units, tiles_p, tiles, grid, whole;
+    int q_tiles, unit_rows, slot_rows;
+};
+
 struct Kv4Plan {
-    int n_split;
+    bool tc, ok;
+    int n_split;                 // CUDA-core kernel: parts the keys are split into
+    Kv4Work w;
     size_t err, part_l, part_o, total;
 };
+
+constexpr int KV4_SMS = 148;
+// A cut costs a pass over the partial results (about 4 us, as long as four steps of
+// 1 us each); whole units are taken where the even share is not that much shorter.
+constexpr int KV4_CUT_STEPS = 4;
 
 inline Kv4Plan kv4_plan(const qi21_config &c, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
     Kv4Plan p{};
     const int64_t keys = P + n_tail, H = c.n_heads;
-    // CUDA-core kernel: CTAs of 32 query rows; two CTAs an SM of 148, at least 64 keys each
-    const int64_t ctas = (n_q + 31) / 32 * H * B;
-    int64_t n = (2 * 148 + ctas - 1) / ctas;
-    if (n > (keys + 63) / 64) n = (keys + 63) / 64;
-    p.n_split = (int)(n < 1 ? 1 : n);
-    const size_t rows = p.n_split > 1 ? (size_t)(B * H * n_q) * p.n_split : 0;
+    size_t rows = 0;             // rows of partial results
+    p.ok = true;
+    p.tc = c.dtype == QI21_DTYPE_BF16 && tc_enabled();
+    if (p.tc) {
+        const int64_t ur = n_q <= 128 ? 128 : 256, qt = (n_q + ur - 1) / ur, units = B * H * qt;
+        const int64_t tp = (P + 127) / 128, tiles = tp + (n_tail + 127) / 128, steps = units * tiles;
+        const int64_t grid = steps < KV4_SMS ? steps : KV4_SMS;
+        const int64_t grid_w = units < KV4_SMS ? units : KV4_SMS;
+        p.w.whole = (units + grid_w - 1) / grid_w * tiles <= (steps + grid - 1) / grid + KV4_CUT_STEPS;
+        p.w.units = (int)units;
+        p.w.tiles_p = (int)tp;
+        p.w.tiles = (int)tiles;
+        p.w.grid = (int)(p.w.whole ? grid_w : grid);
+        p.w.q_tiles = (int)qt;
+        p.w.unit_rows = (int)ur;
+        p.w.slot_rows = (int)(qt == 1 ? n_q : ur);
+        if (units > INT32_MAX) p.ok = false;
+        rows = p.w.whole ? 0 : (size_t)2 * p.w.grid * p.w.slot_rows;
+    } else {
+        // CTAs of 32 query rows; two CTAs an SM, at least 64 keys each
+        const int64_t ctas = (n_q + 31) / 32 * H * B;
+        int64_t n = (2 * KV4_SMS + ctas - 1) / ctas;
+        if (n > (keys + 63) / 64) n = (keys + 63) / 64;
+        p.n_split = (int)(n < 1 ? 1 : n);
+        if (B * p.n_split > 65535) p.ok = false;
+        rows = p.n_split > 1 ? (size_t)(B * H * n_q) * p.n_split : 0;
+    }
     p.part_l = 256;
     p.part_o = p.part_l + align256(rows * 4);
     p.total = p.part_o + align256(rows * 4 * c.head_dim);

@@ -2,6 +2,7 @@
 // (included by qi21_api.cu; the kernels are in qi21_kv4.cuh).
 #pragma once
 #include "qi21_kv4.cuh"
+#include "qi21_kv4_attn_tc.cuh"
 
 namespace qi21 {
 
@@ -76,6 +77,42 @@ static void launch_kv4_attn_simt(Launcher &L, const Kv4AttnArgs &p) {
         });
 }
 
+template <int DH>
+static void launch_kv4_attn_tc(Launcher &L, const Kv4AttnArgs &a, const Kv4Plan &plan) {
+    const uint64_t d = (uint64_t)a.c.H * DH, n_q = a.n_q, nt = a.n_tail > 0 ? a.n_tail : n_q;
+    CUtensorMap q, k, v;
+    // without a tail its maps are never used; they only have to be valid
+    if (!make_map4(&q, a.q, d, n_q, a.B, 1, d, n_q * d, a.B * n_q * d) ||
+        !make_map4(&k, a.n_tail > 0 ? a.k_tail : a.q, d, nt, a.B, 1, d, nt * d, a.B * nt * d) ||
+        !make_map4(&v, a.n_tail > 0 ? a.v_tail : a.q, d, nt, a.B, 1, d, nt * d, a.B * nt * d)) {
+        L.status = QI21_ERR_CUDA;
+        return;
+    }
+    Kv4TcArgs p{};
+    p.a = a;
+    p.w = plan.w;
+    p.part_l = a.part_l;
+    p.part_o = a.part_o;
+    using C = Kv4AttnCfg<DH>;
+    auto go = [&](auto *kernel, DeviceFlags &attr) {
+        smem_opt_in(kernel, (int)C::SMEM, attr);
+        L.run("kv4_attn", [&] {
+            launch_dep(kernel, dim3(p.w.grid), dim3(C::THREADS), C::SMEM, L.st, nullptr, q, k, v, p);
+        });
+    };
+    if (p.w.unit_rows == 128) {
+        static DeviceFlags attr;
+        go(k_kv4_attn_tc<DH, true>, attr);
+    } else {
+        static DeviceFlags attr;
+        go(k_kv4_attn_tc<DH, false>, attr);
+    }
+    if (!p.w.whole && p.w.grid > 1)
+        L.run("kv4_join", [&] {
+            launch_dep(k_kv4_join<DH>, dim3((p.w.slot_rows + 7) / 8, p.w.grid - 1), dim3(256), 0, L.st, nullptr, p);
+        });
+}
+
 // Attention of one layer; ws: the region that kv4_plan() lays out.
 template <typename T>
 static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_kv4_cache &k, int layer, const void *q,
@@ -101,6 +138,13 @@ static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_k
     p.part_o = (float *)(ws + plan.part_o);
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
+    if (plan.tc) {
+        if (c.head_dim == 64)
+            launch_kv4_attn_tc<64>(L, p, plan);
+        else
+            launch_kv4_attn_tc<128>(L, p, plan);
+        return;
+    }
     switch (c.head_dim) {
         case 32: launch_kv4_attn_simt<T, 32>(L, p); break;
         case 64: launch_kv4_attn_simt<T, 64>(L, p); break;
@@ -153,7 +197,7 @@ static qi21_status check_kv4_queries(const qi21_config *c, const qi21_kv4_cache 
     if (k->batch != B && k->batch != 1) return QI21_ERR_CACHE_STATE;
     // one 32-bit index holds every query row, and every key of an item
     if ((int64_t)B * n_q > INT32_MAX - 256 || (int64_t)k->n_prefix + n_tail > INT32_MAX - 256) return QI21_ERR_SHAPE;
-    if ((int64_t)B * kv4_plan(*c, B, n_q, k->n_prefix, n_tail).n_split > 65535) return QI21_ERR_SHAPE;
+    if (!kv4_plan(*c, B, n_q, k->n_prefix, n_tail).ok) return QI21_ERR_SHAPE;
     return QI21_OK;
 }
 
