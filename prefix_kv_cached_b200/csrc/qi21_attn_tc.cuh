@@ -59,6 +59,16 @@ struct AttnParams {
     int shared_tiles, prefix_len, tgt_len, tgt_row0;
 };
 
+// Further parameters of the two-buffer form (EXT): the prefix keys are rows of one
+// K/V buffer, whose items may have lengths of their own, the tail keys rows of
+// another; a row without any key gives 0, a NaN score a NaN row, and the
+// log-sum-exp of each row can be had.
+struct AttnExt {
+    const int *prefix_lens;   // [items of the prefix buffer] (clamped to 0 .. prefix_len) or null
+    int one_prefix;           // every item reads prefix item 0
+    float *lse;               // [H][B][Mq] natural log, or null
+};
+
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -163,10 +173,47 @@ constexpr float kRescaleLog2 = 8.0f;
 // 4th -5 %, every 2nd +6 %, against the scalar MUFU-only softmax.
 constexpr int kPolyEvery = 8;
 
-template <int DH>
-__global__ void __launch_bounds__(320, 1)
-    k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-              const __grid_constant__ CUtensorMap tmV, AttnParams p) {
+// 2^x for a pair as ex2_poly2 does it, with a polynomial of degree DEG
+// (exp2_poly_fit.py's fit of that degree): max relative error 4e-6 (DEG 4) and 2e-7
+// (DEG 5) against ex2_poly2's 1.1e-4, which would show in the log-sum-exp of a row
+// that one key dominates. Inputs below -127 give +0.
+template <int DEG>
+__device__ __forceinline__ void ex2_poly2_deg(float x0, float x1, float &e0, float &e1) {
+    const uint64_t x = f2_pack(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f);   // 1.5 * 2^23: t's low bits hold rint(x)
+    const uint64_t t = f2_add(x, magic);
+    const uint64_t f = f2_sub(x, f2_sub(t, magic));
+    auto two = [](float v) { return f2_pack(v, v); };
+    uint64_t q;
+    if (DEG == 4) {
+        q = f2_fma(two(0.009600395f), f, two(0.055916894f));
+        q = f2_fma(q, f, two(0.24023719f));
+        q = f2_fma(q, f, two(0.69312197f));
+    } else {
+        q = f2_fma(two(0.0013218672f), f, two(0.009671698f));
+        q = f2_fma(q, f, two(0.05550893f));
+        q = f2_fma(q, f, two(0.24022238f));
+        q = f2_fma(q, f, two(0.6931469f));
+    }
+    q = f2_fma(q, f, two(1.0f));
+    float p0, p1, t0, t1;
+    f2_unpack(q, p0, p1);
+    f2_unpack(t, t0, t1);
+    e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+    e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
+// max of three, NaN if any is
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+template <int DH, bool EXT>
+__device__ __forceinline__ void attn_tc_body(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                             const CUtensorMap &tmKt, const CUtensorMap &tmVt, const AttnParams &p,
+                                             const AttnExt &x) {
     using namespace sm100;
     using C = AttnCfg<DH>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -222,25 +269,31 @@ __global__ void __launch_bounds__(320, 1)
     tc_fence_after();
     pdl_launch_dependents();
     pdl_wait();
+    int plen = p.prefix_len;                       // EXT: prefix rows of this item
+    if (EXT && x.prefix_lens) plen = min(max(x.prefix_lens[x.one_prefix ? 0 : b], 0), p.prefix_len);
+    const int p_tiles = EXT ? (plen + C::BK - 1) / C::BK : p.shared_tiles;
     // keys this CTA needs: the largest limit over its query rows
-    if (threadIdx.x >= 64 && threadIdx.x < 64 + C::BQ) {
+    if (!EXT && threadIdx.x >= 64 && threadIdx.x < 64 + C::BQ) {
         const int row = q0 + (threadIdx.x - 64);
         int lim = 0;
         if (row < p.Mq) lim = p.kv_limit ? min(p.kv_limit[row], p.kv_len) : p.kv_len;
         atomicMax(kv_end_s, lim);
     }
-    __syncthreads();
+    if (!EXT) __syncthreads();
     const uint32_t tmem_base = *tmem_slot;
     const int kv_end = *kv_end_s;
-    const int T = p.shared_tiles > 0 ? p.shared_tiles + (p.tgt_len + C::BK - 1) / C::BK
-                                     : (kv_end + C::BK - 1) / C::BK;
+    const int T = EXT || p.shared_tiles > 0 ? p_tiles + (p.tgt_len + C::BK - 1) / C::BK
+                                            : (kv_end + C::BK - 1) / C::BK;
     const int TA = (T + 1) >> 1, TB = T >> 1;     // tiles of half A and half B
     // row and item coordinates of key tile t in the K/V tensor maps
     auto tile_row = [&](int t) -> int {
+        if (EXT) return (t < p_tiles ? t : t - p_tiles) * C::BK;
         if (p.shared_tiles == 0) return t * C::BK;
         return t < p.shared_tiles ? t * C::BK : p.tgt_row0 + b * p.tgt_len + (t - p.shared_tiles) * C::BK;
     };
-    const int kv_item = p.shared_tiles > 0 ? 0 : b;
+    const int kv_item = EXT ? (x.one_prefix ? 0 : b) : (p.shared_tiles > 0 ? 0 : b);
+    // the tensor map and item of tile t
+    auto tail = [&](int t) -> bool { return EXT && t >= p_tiles; };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producers
@@ -248,17 +301,18 @@ __global__ void __launch_bounds__(320, 1)
         if (lane == 0 && T > 0) {
             const uint32_t qb = smem_u32(q_full);
             mbar_arrive_expect_tx(qb, C::Q_BYTES);
-            for (int x = 0; x < C::BOXES; ++x)
-                tma_load_4d(smem_u32(smem + C::OFF_Q + x * (C::BQ * 128)), &tmQ, qb, hh * DH + x * 64,
-                            b * p.Mq + q0, 0, 0);
+            for (int bx = 0; bx < C::BOXES; ++bx)
+                tma_load_4d(smem_u32(smem + C::OFF_Q + bx * (C::BQ * 128)), &tmQ, qb, hh * DH + bx * 64,
+                            EXT ? q0 : b * p.Mq + q0, EXT ? b : 0, 0);
             for (int n = 0; n < T; ++n) {
                 const int s = n % C::SK, tile = (n & 1) ? TA + (n >> 1) : (n >> 1);
                 if (!mbar_wait(smem_u32(&k_empty[s]), ((n / C::SK) & 1) ^ 1, abort_flag, p.err)) break;
                 const uint32_t kb = smem_u32(&k_full[s]);
                 mbar_arrive_expect_tx(kb, C::KV_BYTES);
-                for (int x = 0; x < C::BOXES; ++x)
-                    tma_load_4d(smem_u32(smem + C::OFF_K + s * C::KV_BYTES + x * (C::BK * 128)), &tmK, kb,
-                                hh * DH + x * 64, tile_row(tile), kv_item, p.layer);
+                for (int bx = 0; bx < C::BOXES; ++bx)
+                    tma_load_4d(smem_u32(smem + C::OFF_K + s * C::KV_BYTES + bx * (C::BK * 128)),
+                                tail(tile) ? &tmKt : &tmK, kb, hh * DH + bx * 64, tile_row(tile),
+                                tail(tile) ? b : kv_item, p.layer);
             }
         } else if (lane == 1 && T > 0) {
             for (int n = 0; n < T; ++n) {
@@ -266,9 +320,10 @@ __global__ void __launch_bounds__(320, 1)
                 if (!mbar_wait(smem_u32(&v_empty[s]), ((n / C::SV) & 1) ^ 1, abort_flag, p.err)) break;
                 const uint32_t vb = smem_u32(&v_full[s]);
                 mbar_arrive_expect_tx(vb, C::KV_BYTES);
-                for (int x = 0; x < C::BOXES; ++x)
-                    tma_load_4d(smem_u32(smem + C::OFF_V + s * C::KV_BYTES + x * (C::BK * 128)), &tmV, vb,
-                                hh * DH + x * 64, tile_row(tile), kv_item, p.layer);
+                for (int bx = 0; bx < C::BOXES; ++bx)
+                    tma_load_4d(smem_u32(smem + C::OFF_V + s * C::KV_BYTES + bx * (C::BK * 128)),
+                                tail(tile) ? &tmVt : &tmV, vb, hh * DH + bx * 64, tile_row(tile),
+                                tail(tile) ? b : kv_item, p.layer);
             }
         }
     } else if (warp == 1) {
@@ -385,11 +440,11 @@ __global__ void __launch_bounds__(320, 1)
             // keys of this tile and the first masked one
             const int t = tile0 + j;
             int key0 = t * C::BK, klim = lim;
-            if (p.shared_tiles > 0) {
-                if (t < p.shared_tiles) {
-                    klim = min(lim, p.prefix_len);
+            if (EXT || p.shared_tiles > 0) {
+                if (t < p_tiles) {
+                    klim = EXT ? plen : min(lim, p.prefix_len);
                 } else {
-                    key0 = (t - p.shared_tiles) * C::BK;
+                    key0 = (t - p_tiles) * C::BK;
                     klim = p.tgt_len;
                 }
             }
@@ -400,12 +455,23 @@ __global__ void __launch_bounds__(320, 1)
             }
             // row max: three-input max over pairs, four independent chains
             float m4[4];
+            float mx;
+            if (EXT) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(sv[0][2 * i], sv[0][2 * i + 1]);
+                for (int i = 0; i < 4; ++i) m4[i] = -INFINITY;
 #pragma unroll
-            for (int i = 8; i < 128; i += 2) m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], sv[i >> 5][i & 31],
-                                                                      sv[i >> 5][(i + 1) & 31]);
-            const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                for (int i = 0; i < 128; i += 2)
+                    m4[(i >> 1) & 3] = fmax3_nan(m4[(i >> 1) & 3], sv[i >> 5][i & 31], sv[i >> 5][(i + 1) & 31]);
+                mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+                if (mx != mx) l_run = mx;      // the polynomial exponential would lose a NaN score
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m4[i] = fmaxf(sv[0][2 * i], sv[0][2 * i + 1]);
+#pragma unroll
+                for (int i = 8; i < 128; i += 2)
+                    m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], sv[i >> 5][i & 31], sv[i >> 5][(i + 1) & 31]);
+                mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+            }
             // move the running max only when this tile raises it by more than 2^8
             const bool first = (m_run == -INFINITY);
             const bool grow = first || (mx - m_run) * c > kRescaleLog2;
@@ -434,7 +500,10 @@ __global__ void __launch_bounds__(320, 1)
                     float x0, x1, e0, e1;     // x = S c - m c, one f32x2 FMA for the pair (masked: -inf -> 0)
                     f2_unpack(f2_fma(f2_pack(sv[cc][2 * q], sv[cc][2 * q + 1]), c2, nmc2), x0, x1);
                     if ((cc * 16 + q) % kPolyEvery == kPolyEvery - 1) {
-                        ex2_poly2(x0, x1, e0, e1);
+                        if (EXT)
+                            ex2_poly2_deg<4>(x0, x1, e0, e1);
+                        else
+                            ex2_poly2(x0, x1, e0, e1);
                     } else {
                         e0 = ex2_approx(x0);
                         e1 = ex2_approx(x1);
@@ -481,7 +550,11 @@ __global__ void __launch_bounds__(320, 1)
             if (m == -INFINITY) m = 0.f;
             const float wA = ex2_approx((mA - m) * c);
             const float wB = TB > 0 ? ex2_approx((mB - m) * c) : 0.f;
-            const float inv = 1.f / (lA * wA + lB * wB);
+            const float l = lA * wA + lB * wB;
+            const float inv = EXT && l == 0.f ? 0.f : 1.f / l;
+            if (EXT && x.lse && h == 0 && row < p.Mq)
+                x.lse[((size_t)hh * gridDim.z + b) * p.Mq + row] =
+                    l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
             const float fA = wA * inv, fB = wB * inv;
             bf16 *dst = p.out + ((size_t)b * p.Mq + row) * p.d + hh * DH + h * (DH / 2);
 #pragma unroll
@@ -500,6 +573,11 @@ __global__ void __launch_bounds__(320, 1)
                 }
                 if (row < p.Mq) store_bf16x32(dst + cc * 32, oa);
             }
+        } else if (EXT && T == 0 && row < p.Mq) {          // no key at all
+            bf16 *dst = p.out + ((size_t)b * p.Mq + row) * p.d + hh * DH + h * (DH / 2);
+            const float zero[32] = {};
+            for (int cc = 0; cc < DH / 64; ++cc) store_bf16x32(dst + cc * 32, zero);
+            if (x.lse && h == 0) x.lse[((size_t)hh * gridDim.z + b) * p.Mq + row] = -INFINITY;
         }
     }
     tc_fence_before();
@@ -508,6 +586,24 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
     }
+}
+
+template <int DH>
+__global__ void __launch_bounds__(320, 1)
+    k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnParams p) {
+    attn_tc_body<DH, false>(tmQ, tmK, tmV, tmK, tmV, p, AttnExt{});
+}
+
+// The two-buffer form: q [B][Mq][d]; tmK, tmV over the prefix buffer, tmKt, tmVt over
+// the tail rows [B][tgt_len][d].
+template <int DH>
+__global__ void __launch_bounds__(320, 1)
+    k_attn_tc_ext(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
+                  const __grid_constant__ CUtensorMap tmVt, const __grid_constant__ AttnParams p,
+                  const __grid_constant__ AttnExt x) {
+    attn_tc_body<DH, true>(tmQ, tmK, tmV, tmKt, tmVt, p, x);
 }
 
 }  // namespace qi21

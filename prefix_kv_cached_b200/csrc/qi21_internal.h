@@ -108,11 +108,13 @@ struct Kv4Work {
     int q_tiles, unit_rows, slot_rows;
 };
 
+//   expanded: the layer's prefix rows are first written out in bf16 (expand, [K|V]
+//   [items][Pp][d]) and the attention reads those.
 struct Kv4Plan {
-    bool tc, ok;
+    bool tc, expanded, ok;
     int n_split;                 // CUDA-core kernel: parts the keys are split into
     Kv4Work w;
-    size_t err, part_l, part_o, total;
+    size_t err, part_l, part_o, expand, total;
 };
 
 constexpr int KV4_SMS = 148;
@@ -120,7 +122,17 @@ constexpr int KV4_SMS = 148;
 // 1 us each); whole units are taken where the even share is not that much shorter.
 constexpr int KV4_CUT_STEPS = 4;
 
-inline Kv4Plan kv4_plan(const qi21_config &c, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
+// From this many query rows on, where the 128-row query tiles fill the SMs, the
+// prefix is expanded once instead of once for every 256 rows. us, expanded / not (32
+// heads of 128, P 4608, as many tail keys as rows): 4096 rows 462 / 655, 2048 rows
+// 205 / 294, 1024 rows 117 / 153, 512 rows 103 / 89; P 33792: 1024 rows 620 / 645,
+// 512 rows 352 / 331.
+#ifndef KV4_EXPAND_ROWS
+#define KV4_EXPAND_ROWS 1024
+#endif
+constexpr int KV4_EXPAND_WAVES = 1;
+
+inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
     Kv4Plan p{};
     const int64_t keys = P + n_tail, H = c.n_heads;
     size_t rows = 0;             // rows of partial results
@@ -140,7 +152,9 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t B, int64_t n_q, int64_t P,
         p.w.unit_rows = (int)ur;
         p.w.slot_rows = (int)(qt == 1 ? n_q : ur);
         if (units > INT32_MAX) p.ok = false;
-        rows = p.w.whole ? 0 : (size_t)2 * p.w.grid * p.w.slot_rows;
+        p.expanded = n_q >= KV4_EXPAND_ROWS && B * H * ((n_q + 127) / 128) >= KV4_EXPAND_WAVES * KV4_SMS;
+        if (p.expanded && (B > 65535 || (n_q + 127) / 128 > INT32_MAX)) p.ok = false;
+        rows = p.w.whole || p.expanded ? 0 : (size_t)2 * p.w.grid * p.w.slot_rows;
     } else {
         // CTAs of 32 query rows; two CTAs an SM, at least 64 keys each
         const int64_t ctas = (n_q + 31) / 32 * H * B;
@@ -152,7 +166,9 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t B, int64_t n_q, int64_t P,
     }
     p.part_l = 256;
     p.part_o = p.part_l + align256(rows * 4);
-    p.total = p.part_o + align256(rows * 4 * c.head_dim);
+    p.expand = p.part_o + align256(rows * 4 * c.head_dim);
+    p.total = p.expand;
+    if (p.expanded) p.total += align256((size_t)2 * items * ((P + 127) / 128 * 128) * c.d_model * 2);
     return p;
 }
 
@@ -167,7 +183,7 @@ inline Kv4StepLayout kv4_step_layout(const qi21_config &c, int64_t B, int64_t P,
     Kv4StepLayout s{};
     s.lse = ws_layout(c, B, 0, N).total;
     s.kv4 = s.lse + align256(sizeof(float) * (size_t)c.n_heads * B * N);
-    s.total = s.kv4 + kv4_plan(c, B, N, P, N).total;
+    s.total = s.kv4 + kv4_plan(c, B, B, N, P, N).total;
     return s;
 }
 

@@ -166,25 +166,31 @@ __device__ __forceinline__ float kv4_load_scale(const uint8_t *base, const Kv4Di
         (uint32_t)reinterpret_cast<const uint16_t *>(base + c.scales_off)[row * (c.Dh / KV4_GROUP) + group] << 16);
 }
 
-// The way back: rows [0, len) of every slab in token-major layout, the mapping of
-// k_kv4_quantize.
+// The way back: rows [0, len) of slabs slab0, slab0 + 1, .. in token-major layout,
+// the mapping of k_kv4_quantize. pad: zeros behind them up to a multiple of 128 rows
+// (the tiles of an attention that reads the result).
 template <typename T>
-__global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *__restrict__ base, Kv4Dims c,
-                                                        const int *__restrict__ prefix_len, T *__restrict__ dst,
-                                                        int64_t slab_stride) {
+__global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *__restrict__ base, Kv4Dims c, int slab0,
+                                                        const int *__restrict__ prefix_len, int pad,
+                                                        T *__restrict__ dst, int64_t slab_stride) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int d = c.H * c.Dh, cols = d / 8;
     const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int slab = blockIdx.y;
+    const int slab = slab0 + blockIdx.y;
     const int rows = kv4_len(c, prefix_len, slab % c.B);
     const int64_t quad = u / cols;
     const int col = (int)(u - quad * cols);
     const int h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
     const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp;
+    const int rows_out = pad ? (int)kv4_pad(rows) : rows;
     uint32_t w[KV4_Q_ROWS];
     float s[KV4_Q_ROWS];
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
         const int64_t r = quad * KV4_Q_ROWS + i;
+        w[i] = 0;
+        s[i] = 0.f;
         if (r < rows) {
             w[i] = *reinterpret_cast<const uint32_t *>(base + (row0 + r) * (c.Dh / 2) + j0 / 2);
             s[i] = kv4_load_scale(base, c, row0 + r, j0 / KV4_GROUP);
@@ -193,10 +199,10 @@ __global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *__restric
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
         const int64_t r = quad * KV4_Q_ROWS + i;
-        if (r < rows) {
+        if (r < rows_out) {
             float x[8];
             kv4_values(w[i], s[i], x);
-            store8(dst + slab * slab_stride + r * d + col * 8, x);
+            store8(dst + (int64_t)blockIdx.y * slab_stride + r * d + col * 8, x);
         }
     }
 }

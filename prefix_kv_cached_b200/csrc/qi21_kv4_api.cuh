@@ -57,9 +57,8 @@ template <typename T>
 static void launch_kv4_dequantize(Launcher &L, const qi21_config &c, const qi21_kv4_cache &src,
                                   const qi21_kv_cache &dst) {
     L.run("kv4_dequantize", [&] {
-        k_kv4_dequantize<T><<<kv4_row_grid(c, src), 256, 0, L.st>>>((const uint8_t *)src.base, kv4_dims(src),
-                                                                    src.prefix_len, (T *)dst.base,
-                                                                    kv_slab_rows(dst) * c.d_model);
+        launch_dep(k_kv4_dequantize<T>, kv4_row_grid(c, src), dim3(256), 0, L.st, nullptr, (const uint8_t *)src.base,
+                   kv4_dims(src), 0, src.prefix_len, 0, (T *)dst.base, kv_slab_rows(dst) * c.d_model);
     });
 }
 
@@ -113,12 +112,53 @@ static void launch_kv4_attn_tc(Launcher &L, const Kv4AttnArgs &a, const Kv4Plan 
         });
 }
 
+// Many query rows: the layer's prefix in bf16 first, then the attention over it
+// and the tail.
+template <int DH>
+static void launch_kv4_attn_expanded(Launcher &L, const Kv4AttnArgs &a, const Kv4Plan &plan, char *ws) {
+    const uint64_t d = (uint64_t)a.c.H * DH, n_q = a.n_q, nt = a.n_tail > 0 ? a.n_tail : n_q, pp = a.c.Pp;
+    bf16 *ek = (bf16 *)(ws + plan.expand), *ev = ek + a.c.B * pp * d;
+    const int64_t quads = pp / KV4_Q_ROWS;
+    L.run("kv4_expand", [&] {
+        launch_dep(k_kv4_dequantize<bf16>, dim3((unsigned)((quads * (d / 8) + 255) / 256), 2 * a.c.B), dim3(256), 0,
+                   L.st, nullptr, a.base, a.c, a.layer * 2 * a.c.B, a.prefix_len, 1, ek, (int64_t)(pp * d));
+    });
+    CUtensorMap q, k, v, kt, vt;
+    if (!make_map4(&q, a.q, d, n_q, a.B, 1, d, n_q * d, a.B * n_q * d) ||
+        !make_map4(&k, ek, d, pp, a.c.B, 1, d, pp * d, a.c.B * pp * d) ||
+        !make_map4(&v, ev, d, pp, a.c.B, 1, d, pp * d, a.c.B * pp * d) ||
+        // without a tail its maps are never used; they only have to be valid
+        !make_map4(&kt, a.n_tail > 0 ? a.k_tail : a.q, d, nt, a.B, 1, d, nt * d, a.B * nt * d) ||
+        !make_map4(&vt, a.n_tail > 0 ? a.v_tail : a.q, d, nt, a.B, 1, d, nt * d, a.B * nt * d)) {
+        L.status = QI21_ERR_CUDA;
+        return;
+    }
+    AttnParams p{};
+    p.Mq = a.n_q;
+    p.kv_len = a.c.P + a.n_tail;
+    p.H = a.c.H;
+    p.d = (int)d;
+    p.out = (bf16 *)a.out;
+    p.scale_log2 = a.scale_log2;
+    p.err = a.err;
+    p.prefix_len = a.c.P;
+    p.tgt_len = a.n_tail;
+    const AttnExt x{a.prefix_len, a.shared, a.lse};
+    using Cf = AttnCfg<DH>;
+    static DeviceFlags attr;
+    smem_opt_in(k_attn_tc_ext<DH>, (int)Cf::SMEM, attr);
+    L.run("kv4_attn", [&] {
+        launch_dep(k_attn_tc_ext<DH>, dim3((p.Mq + Cf::BQ - 1) / Cf::BQ, p.H, a.B), dim3(Cf::THREADS), Cf::SMEM, L.st,
+                   nullptr, q, k, v, kt, vt, p, x);
+    });
+}
+
 // Attention of one layer; ws: the region that kv4_plan() lays out.
 template <typename T>
 static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_kv4_cache &k, int layer, const void *q,
                                  int B, int n_q, const void *k_tail, const void *v_tail, int n_tail, void *out,
                                  float *lse, char *ws, uint32_t *err) {
-    const Kv4Plan plan = kv4_plan(c, B, n_q, k.n_prefix, n_tail);
+    const Kv4Plan plan = kv4_plan(c, k.batch, B, n_q, k.n_prefix, n_tail);
     Kv4AttnArgs p{};
     p.base = (const uint8_t *)k.base;
     p.c = kv4_dims(k);
@@ -138,6 +178,13 @@ static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_k
     p.part_o = (float *)(ws + plan.part_o);
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
+    if (plan.expanded) {
+        if (c.head_dim == 64)
+            launch_kv4_attn_expanded<64>(L, p, plan, ws);
+        else
+            launch_kv4_attn_expanded<128>(L, p, plan, ws);
+        return;
+    }
     if (plan.tc) {
         if (c.head_dim == 64)
             launch_kv4_attn_tc<64>(L, p, plan);
@@ -197,7 +244,7 @@ static qi21_status check_kv4_queries(const qi21_config *c, const qi21_kv4_cache 
     if (k->batch != B && k->batch != 1) return QI21_ERR_CACHE_STATE;
     // one 32-bit index holds every query row, and every key of an item
     if ((int64_t)B * n_q > INT32_MAX - 256 || (int64_t)k->n_prefix + n_tail > INT32_MAX - 256) return QI21_ERR_SHAPE;
-    if (!kv4_plan(*c, B, n_q, k->n_prefix, n_tail).ok) return QI21_ERR_SHAPE;
+    if (!kv4_plan(*c, k->batch, B, n_q, k->n_prefix, n_tail).ok) return QI21_ERR_SHAPE;
     return QI21_OK;
 }
 

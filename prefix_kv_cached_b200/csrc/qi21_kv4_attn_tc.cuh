@@ -91,47 +91,10 @@ __device__ __forceinline__ uint4 kv4_expand(uint32_t w, uint32_t s2, uint32_t of
                       __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
 }
 
-// 2^x for a pair on the FMA pipe as ex2_poly2 does it, with a polynomial of degree
-// DEG (exp2_poly_fit.py's fit of that degree): max relative error 4e-6 (DEG 4) and
-// 2e-7 (DEG 5) against ex2_poly2's 1.1e-4, which would show in the log-sum-exp of a
-// row that one key dominates. Inputs below -127 give +0.
-template <int DEG>
-__device__ __forceinline__ void kv4_ex2_poly2(float x0, float x1, float &e0, float &e1) {
-    const uint64_t x = f2_pack(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-    const uint64_t magic = f2_pack(12582912.f, 12582912.f);   // 1.5 * 2^23: t's low bits hold rint(x)
-    const uint64_t t = f2_add(x, magic);
-    const uint64_t f = f2_sub(x, f2_sub(t, magic));
-    auto two = [](float v) { return f2_pack(v, v); };
-    uint64_t q;
-    if (DEG == 4) {
-        q = f2_fma(two(0.009600395f), f, two(0.055916894f));
-        q = f2_fma(q, f, two(0.24023719f));
-        q = f2_fma(q, f, two(0.69312197f));
-    } else {
-        q = f2_fma(two(0.0013218672f), f, two(0.009671698f));
-        q = f2_fma(q, f, two(0.05550893f));
-        q = f2_fma(q, f, two(0.24022238f));
-        q = f2_fma(q, f, two(0.6931469f));
-    }
-    q = f2_fma(q, f, two(1.0f));
-    float p0, p1, t0, t1;
-    f2_unpack(q, p0, p1);
-    f2_unpack(t, t0, t1);
-    e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-    e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                  : "memory");
-}
-
-// max of three, NaN if any is
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 template <int R>
@@ -513,7 +476,7 @@ __global__ void __launch_bounds__(512, 1)
                         float x0, x1, e0, e1;
                         f2_unpack(f2_fma(f2_pack(sv[cc][2 * q], sv[cc][2 * q + 1]), c2, nmc2), x0, x1);
                         if ((cc * 16 + q) % kPolyEvery == kPolyEvery - 1) {
-                            kv4_ex2_poly2<4>(x0, x1, e0, e1);
+                            ex2_poly2_deg<4>(x0, x1, e0, e1);
                         } else {
                             e0 = ex2_approx(x0);
                             e1 = ex2_approx(x1);

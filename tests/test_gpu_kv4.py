@@ -197,6 +197,8 @@ ATT = [
     (2, 128, 1, 1, 128, 256, 128, None), (2, 128, 1, 1, 127, 257, 129, None), (8, 128, 1, 1, 1100, 64, 640, None),
     (4, 64, 2, 2, 383, 128, 0, [382, 3]), (2, 128, 1, 1, 40, 17, 1000, None), (2, 128, 2, 2, 100, 520, 30, [-5, 1000]),
     (32, 128, 1, 1, 640, 24, 5, None), (4, 64, 5, 5, 90, 2, 300, [0, 0, 90, 1, 64]),
+    (16, 64, 5, 5, 200, 1030, 50, [200, 0, 130, 1, 77]), (32, 128, 1, 3, 140, 1024, 0, None),
+    (16, 64, 5, 5, 130, 1024, 0, [0, 130, 2, 128, 129]), (32, 128, 2, 2, 257, 1153, 300, None),
 ]
 
 
