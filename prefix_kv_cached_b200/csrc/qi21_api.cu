@@ -927,6 +927,8 @@ extern "C" qi21_status qi21_cached_step_kv4(const qi21_config *c, const qi21_wei
     if (s) return s;
     if ((s = check_weights(w, false))) return s;
     if ((s = check_kv4_queries(c, cache, B, N, N))) return s;
+    if (scores && !kv4_score_plan(*c, cache->batch, cache->batch == 1 ? (int64_t)B * N : N, cache->n_prefix).ok)
+        return QI21_ERR_SHAPE;
     if (!al16(x_k) || !al16(cos_sin_target) || !al16(mod_row_target) || !al16(scale_final) || !al16(v_out) ||
         ((uintptr_t)scores & 15) || !al16(ws))
         return QI21_ERR_INVALID_ARG;
@@ -1023,7 +1025,10 @@ extern "C" qi21_status qi21_kv4_scores(const qi21_config *c, const qi21_kv4_cach
     if (layer < 0 || layer >= c->n_layers || !al16(q) || !al16(lse) || ((uintptr_t)scores_in & 15) ||
         !al16(scores_out) || !al16(ws))
         return QI21_ERR_INVALID_ARG;
-    if (ws_bytes < kv4_plan(*c, B, B, n_q, cache->n_prefix, 0).total) return QI21_ERR_WORKSPACE_TOO_SMALL;
+    const Kv4ScorePlan plan = kv4_score_plan(*c, cache->batch, cache->batch == 1 ? (int64_t)B * n_q : n_q,
+                                             cache->n_prefix);
+    if (!plan.ok) return QI21_ERR_SHAPE;
+    if (ws_bytes < plan.total) return QI21_ERR_WORKSPACE_TOO_SMALL;
     Launcher L((cudaStream_t)stream);
     if (c->dtype == QI21_DTYPE_BF16)
         launch_kv4_scores<bf16>(L, *c, *cache, layer, q, B, n_q, lse, scores_in, scores_out, (char *)ws,

@@ -271,7 +271,7 @@ extern "C" qi21_status qi21_kv4_cache_init(qi21_kv4_cache *cache, void *base, co
 
 extern "C" size_t qi21_kv4_workspace_bytes(const qi21_config *c, int32_t B, int32_t n_q, int32_t P, int32_t n_tail) {
     if (!qi21_config_ok(c) || !qi21::kv4_head_dim_ok(*c) || B <= 0 || n_q <= 0 || P <= 0 || n_tail < 0) return 0;
-    return qi21::kv4_plan(*c, B, B, n_q, P, n_tail).total;
+    return qi21::kv4_ops_workspace(*c, B, n_q, P, n_tail);
 }
 
 extern "C" size_t qi21_kv4_step_workspace_bytes(const qi21_config *c, int32_t B, int32_t P, int32_t N) {

@@ -172,6 +172,42 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t 
     return p;
 }
 
+// Plan of the accumulated weights: the tensor-core kernel's CTAs take one 128-key
+// tile each; where those are fewer than two an SM, the query tiles are split, whose
+// sums lie in the workspace.
+struct Kv4ScorePlan {
+    bool tc, ok;
+    int q_tiles, n_split;
+    size_t part, total;
+};
+
+// rows: query rows per cache item
+inline Kv4ScorePlan kv4_score_plan(const qi21_config &c, int64_t items, int64_t rows, int64_t P) {
+    Kv4ScorePlan p{};
+    p.tc = c.dtype == QI21_DTYPE_BF16 && tc_enabled();
+    p.n_split = 1;
+    p.ok = items <= 65535;
+    p.part = p.total = 256;
+    if (p.tc) {
+        const int64_t tp = (P + 127) / 128, ctas = tp * c.n_heads * items, qt = (rows + 127) / 128;
+        int64_t n = (2 * KV4_SMS) / ctas;
+        if (n > qt) n = qt;
+        p.n_split = (int)(n < 1 ? 1 : n);
+        p.q_tiles = (int)qt;
+        if (items * p.n_split > 65535) p.ok = false;
+        if (p.n_split > 1) p.total += align256((size_t)p.n_split * items * c.n_heads * tp * 128 * 4);
+    }
+    return p;
+}
+
+// Workspace of the attention, and of the weights over a cache of B items or of one.
+inline size_t kv4_ops_workspace(const qi21_config &c, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
+    size_t n = kv4_plan(c, B, B, n_q, P, n_tail).total;
+    const size_t a = kv4_score_plan(c, B, n_q, P).total, one = kv4_score_plan(c, 1, B * n_q, P).total;
+    if (n < a) n = a;
+    return n < one ? one : n;
+}
+
 // Workspace of the cached step over a 4-bit cache: that of a cached step without
 // prefix (its full-recompute K/V region holds the target K/V), the rows'
 // log-sum-exps, and the attention's partial results.
@@ -183,7 +219,7 @@ inline Kv4StepLayout kv4_step_layout(const qi21_config &c, int64_t B, int64_t P,
     Kv4StepLayout s{};
     s.lse = ws_layout(c, B, 0, N).total;
     s.kv4 = s.lse + align256(sizeof(float) * (size_t)c.n_heads * B * N);
-    s.total = s.kv4 + kv4_plan(c, B, B, N, P, N).total;
+    s.total = s.kv4 + kv4_ops_workspace(c, B, N, P, N);
     return s;
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 #include "qi21_kv4.cuh"
 #include "qi21_kv4_attn_tc.cuh"
+#include "qi21_kv4_scores_tc.cuh"
 
 namespace qi21 {
 
@@ -210,6 +211,28 @@ static void launch_kv4_scores_simt(Launcher &L, const Kv4ScoreArgs &p) {
     });
 }
 
+template <int DH>
+static void launch_kv4_scores_tc(Launcher &L, const Kv4ScoreArgs &a, const Kv4ScorePlan &plan, float *part) {
+    const uint64_t d = (uint64_t)a.c.H * DH, n_q = a.n_q;
+    CUtensorMap q;
+    if (!make_map4(&q, a.q, d, n_q, a.c.B, 1, d, n_q * d, a.c.B * n_q * d)) {
+        L.status = QI21_ERR_CUDA;
+        return;
+    }
+    Kv4ScoreTcArgs p{a, plan.q_tiles, plan.n_split, part};
+    using C = Kv4ScoreCfg<DH>;
+    static DeviceFlags attr;
+    smem_opt_in(k_kv4_scores_tc<DH>, (int)C::SMEM, attr);
+    L.run("kv4_scores", [&] {
+        launch_dep(k_kv4_scores_tc<DH>, dim3(a.c.Pp / 128, a.c.H, a.c.B * p.n_split), dim3(C::THREADS), C::SMEM, L.st,
+                   nullptr, q, p);
+    });
+    if (p.n_split > 1)
+        L.run("kv4_scores_reduce", [&] {
+            launch_dep(k_kv4_scores_reduce, dim3((a.c.P + 255) / 256, a.c.H, a.c.B), dim3(256), 0, L.st, nullptr, p);
+        });
+}
+
 template <typename T>
 static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_cache &k, int layer, const void *q,
                               int B, int n_q, const float *lse, const float *in, float *out, char *ws,
@@ -226,6 +249,14 @@ static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_
     p.out = out;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
+    const Kv4ScorePlan plan = kv4_score_plan(c, k.batch, p.n_q, k.n_prefix);
+    if (plan.tc) {
+        if (c.head_dim == 64)
+            launch_kv4_scores_tc<64>(L, p, plan, (float *)(ws + plan.part));
+        else
+            launch_kv4_scores_tc<128>(L, p, plan, (float *)(ws + plan.part));
+        return;
+    }
     switch (c.head_dim) {
         case 32: launch_kv4_scores_simt<T, 32>(L, p); break;
         case 64: launch_kv4_scores_simt<T, 64>(L, p); break;

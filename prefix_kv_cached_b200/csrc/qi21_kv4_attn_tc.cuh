@@ -106,26 +106,25 @@ __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// Expand one 128-row tile of codes from a staging slot into the swizzled operand
-// buffer at dst (boxes of 64 dims, rows of 128 bytes). 128 threads; rows from
-// n_rows on become zeros (their scale is taken as 0). A quarter warp covers four
-// rows and two groups: its eight 16-byte stores fall into eight different chunks
-// of the swizzle.
-template <int DH>
-__device__ __forceinline__ void kv4_expand_tile(uint8_t *dst, const uint8_t *stage, int n_rows) {
-    using C = Kv4AttnCfg<DH>;
-    const int t = threadIdx.x & 127, lane = t & 31, warp = t >> 5;
-    constexpr int RPW = 32 / C::G;                 // rows of a warp at a time
-    const int g = C::G == 4 ? (lane & 1) | ((lane >> 2) & 2) : lane & 1;
-    const int r0 = C::G == 4 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : ((lane >> 1) & 3) | ((lane >> 3) << 2);
+// Expand one 128-row tile of codes (rows of DH/2 bytes) into the swizzled operand
+// buffer at dst (boxes of 64 dims, rows of 128 bytes) with W warps; rows from n_rows
+// on become zeros (their scale is taken as 0). A quarter warp covers four rows and
+// two groups: its eight 16-byte stores fall into eight different chunks of the
+// swizzle.
+template <int DH, int W>
+__device__ __forceinline__ void kv4_expand_tile(uint8_t *dst, const uint8_t *codes, const uint8_t *scales, int n_rows,
+                                                int warp, int lane) {
+    constexpr int G = DH / KV4_GROUP, RPW = 32 / G, ROWS = 128 / W;     // rows of a warp at a time, and in all
+    const int g = G == 4 ? (lane & 1) | ((lane >> 2) & 2) : lane & 1;
+    const int r0 = G == 4 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : ((lane >> 1) & 3) | ((lane >> 3) << 2);
 #pragma unroll
-    for (int it = 0; it < 32 / RPW; ++it) {
-        const int r = warp * 32 + it * RPW + r0;
-        const uint4 w = *reinterpret_cast<const uint4 *>(stage + r * (DH / 2) + g * 16);
-        uint32_t s = *reinterpret_cast<const uint16_t *>(stage + C::CODE_BYTES + (r * C::G + g) * 2);
+    for (int it = 0; it < ROWS / RPW; ++it) {
+        const int r = warp * ROWS + it * RPW + r0;
+        const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * (DH / 2) + g * 16);
+        uint32_t s = *reinterpret_cast<const uint16_t *>(scales + (r * G + g) * 2);
         if (r >= n_rows) s = 0;
         const uint32_t s2 = kv4_scale_pair(s), off2 = kv4_offset_pair(s2);
-        uint8_t *row = dst + (g >> 1) * (C::BK * 128) + r * 128;
+        uint8_t *row = dst + (g >> 1) * (128 * 128) + r * 128;
         const int c0 = (g & 1) * 4, x = r & 7;
         *reinterpret_cast<uint4 *>(row + (((c0 + 0) ^ x) << 4)) = kv4_expand(w.x, s2, off2);
         *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ x) << 4)) = kv4_expand(w.y, s2, off2);
@@ -387,7 +386,11 @@ __global__ void __launch_bounds__(512, 1)
                     if (tile < p.w.tiles_p) {
                         const uint32_t ss = st % C::NS;
                         if (!(ok = wait_all(&st_full[ss], (st / C::NS) & 1))) break;
-                        kv4_expand_tile<DH>(dst, smem + C::OFF_ST + ss * C::STAGE_BYTES, seg.len - tile * 128);
+                        {
+                            const uint8_t *stage = smem + C::OFF_ST + ss * C::STAGE_BYTES;
+                            kv4_expand_tile<DH, 4>(dst, stage, stage + C::CODE_BYTES, seg.len - tile * 128, warp - 8,
+                                                   lane);
+                        }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
