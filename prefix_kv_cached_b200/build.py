@@ -21,7 +21,7 @@ DEBUG_LIB = os.path.join(HERE, "libqi21_debug.so")
 SOURCES = ["qi21_api.cu", "qi21_noalloc.cu", "qi21_host.cpp"]
 HEADERS = ["qi21_internal.h", "qi21_common.cuh", "qi21_simt.cuh", "qi21_sm100.cuh", "qi21_gemm_tc.cuh",
            "qi21_attn_tc.cuh", "qi21_final_tc.cuh", "qi21_kv4.cuh", "qi21_kv4_attn_tc.cuh",
-           "qi21_kv4_scores_tc.cuh", "qi21_kv4_api.cuh"]
+           "qi21_kv4_scores_tc.cuh", "qi21_kv4_rows.cuh", "qi21_kv4_api.cuh"]
 
 
 def _nvcc() -> str:

@@ -110,9 +110,10 @@ struct Kv4Work {
 
 //   expanded: the layer's prefix rows are first written out in bf16 (expand, [K|V]
 //   [items][Pp][d]) and the attention reads those.
+//   rows: few query rows; CTAs of 8 or 16 rows whose keys are split.
 struct Kv4Plan {
-    bool tc, expanded, ok;
-    int n_split;                 // CUDA-core kernel: parts the keys are split into
+    bool tc, expanded, rows, ok;
+    int n_split;                 // rows and CUDA-core kernels: parts the keys are split into
     Kv4Work w;
     size_t err, part_l, part_o, expand, total;
 };
@@ -131,6 +132,10 @@ constexpr int KV4_CUT_STEPS = 4;
 #define KV4_EXPAND_ROWS 1024
 #endif
 constexpr int KV4_EXPAND_WAVES = 1;
+// Up to this many query rows the few-rows kernel.
+#ifndef KV4_ROWS_MAX
+#define KV4_ROWS_MAX 32
+#endif
 
 inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
     Kv4Plan p{};
@@ -138,7 +143,17 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t 
     size_t rows = 0;             // rows of partial results
     p.ok = true;
     p.tc = c.dtype == QI21_DTYPE_BF16 && tc_enabled();
-    if (p.tc) {
+    if (p.tc && n_q <= KV4_ROWS_MAX) {
+        // two CTAs an SM, at least a 64-key chunk for each of a CTA's four warps
+        p.rows = true;
+        const int64_t tile = n_q <= 8 ? 8 : 16, ctas = (n_q + tile - 1) / tile * H * B;
+        const int64_t chunks = (P + 63) / 64 + (n_tail + 63) / 64;
+        int64_t n = 2 * KV4_SMS / ctas;
+        if (n > (chunks + 3) / 4) n = (chunks + 3) / 4;
+        p.n_split = (int)(n < 1 ? 1 : n);
+        if (B * p.n_split > 65535) p.ok = false;
+        rows = p.n_split > 1 ? (size_t)(B * H * n_q) * p.n_split : 0;
+    } else if (p.tc) {
         const int64_t ur = n_q <= 128 ? 128 : 256, qt = (n_q + ur - 1) / ur, units = B * H * qt;
         const int64_t tp = (P + 127) / 128, tiles = tp + (n_tail + 127) / 128, steps = units * tiles;
         const int64_t grid = steps < KV4_SMS ? steps : KV4_SMS;
@@ -175,8 +190,10 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t 
 // Plan of the accumulated weights: the tensor-core kernel's CTAs take one 128-key
 // tile each; where those are fewer than two an SM, the query tiles are split, whose
 // sums lie in the workspace.
+//   rows: few query rows; n_split is then the parts a head's keys are split into, and
+//   no sum is split.
 struct Kv4ScorePlan {
-    bool tc, ok;
+    bool tc, rows, ok;
     int q_tiles, n_split;
     size_t part, total;
 };
@@ -188,7 +205,13 @@ inline Kv4ScorePlan kv4_score_plan(const qi21_config &c, int64_t items, int64_t 
     p.n_split = 1;
     p.ok = items <= 65535;
     p.part = p.total = 256;
-    if (p.tc) {
+    if (p.tc && rows <= KV4_ROWS_MAX) {
+        p.rows = true;
+        int64_t n = 4 * KV4_SMS / (c.n_heads * items);         // four CTAs an SM
+        const int64_t most = (P + 255) / 256;                  // a 64-key chunk for each warp
+        if (n > most) n = most;
+        p.n_split = (int)(n < 1 ? 1 : n);
+    } else if (p.tc) {
         const int64_t tp = (P + 127) / 128, ctas = tp * c.n_heads * items, qt = (rows + 127) / 128;
         int64_t n = (2 * KV4_SMS) / ctas;
         if (n > qt) n = qt;

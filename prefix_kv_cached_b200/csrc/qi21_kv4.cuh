@@ -523,6 +523,8 @@ __global__ void __launch_bounds__(128) k_kv4_attn_simt(Kv4AttnArgs p) {
 // 0 and -inf. A warp per (item, head, row), in a fixed order. grid (rows / 8, H, B).
 template <typename T, int DH>
 __global__ void __launch_bounds__(256) k_kv4_combine(Kv4AttnArgs p) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
     if (row >= p.n_q) return;
     const int64_t at0 = ((int64_t)b * p.c.H + h) * p.n_split * p.n_q + row;

@@ -3,6 +3,7 @@
 #pragma once
 #include "qi21_kv4.cuh"
 #include "qi21_kv4_attn_tc.cuh"
+#include "qi21_kv4_rows.cuh"
 #include "qi21_kv4_scores_tc.cuh"
 
 namespace qi21 {
@@ -113,6 +114,29 @@ static void launch_kv4_attn_tc(Launcher &L, const Kv4AttnArgs &a, const Kv4Plan 
         });
 }
 
+template <int DH>
+static void launch_kv4_attn_rows(Launcher &L, const Kv4AttnArgs &p) {
+    constexpr size_t smem = Kv4RowsCfg<DH, true>::SMEM;
+    auto go = [&](auto *kernel, int tile, DeviceFlags &attr) {
+        smem_opt_in(kernel, (int)smem, attr);
+        L.run("kv4_attn", [&] {
+            launch_dep(kernel, dim3((p.n_q + tile - 1) / tile, p.c.H, p.B * p.n_split), dim3(32 * KV4R_WARPS), smem, L.st,
+                       nullptr, p);
+        });
+    };
+    if (p.n_q <= 8) {
+        static DeviceFlags attr;
+        go(k_kv4_attn_rows<DH, 1>, 8, attr);
+    } else {
+        static DeviceFlags attr;
+        go(k_kv4_attn_rows<DH, 2>, 16, attr);
+    }
+    if (p.n_split > 1)
+        L.run("kv4_combine", [&] {
+            launch_dep(k_kv4_combine<bf16, DH>, dim3((p.n_q + 7) / 8, p.c.H, p.B), dim3(256), 0, L.st, nullptr, p);
+        });
+}
+
 // Many query rows: the layer's prefix in bf16 first, then the attention over it
 // and the tail.
 template <int DH>
@@ -179,6 +203,13 @@ static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_k
     p.part_o = (float *)(ws + plan.part_o);
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
+    if (plan.rows) {
+        if (c.head_dim == 64)
+            launch_kv4_attn_rows<64>(L, p);
+        else
+            launch_kv4_attn_rows<128>(L, p);
+        return;
+    }
     if (plan.expanded) {
         if (c.head_dim == 64)
             launch_kv4_attn_expanded<64>(L, p, plan, ws);
@@ -233,6 +264,16 @@ static void launch_kv4_scores_tc(Launcher &L, const Kv4ScoreArgs &a, const Kv4Sc
         });
 }
 
+template <int DH>
+static void launch_kv4_scores_rows(Launcher &L, const Kv4ScoreArgs &p, int n_split) {
+    constexpr size_t smem = Kv4RowsCfg<DH, false>::SMEM;
+    static DeviceFlags attr;
+    smem_opt_in(k_kv4_scores_rows<DH>, (int)smem, attr);
+    L.run("kv4_scores", [&] {
+        launch_dep(k_kv4_scores_rows<DH>, dim3(n_split, p.c.H, p.c.B), dim3(32 * KV4R_WARPS), smem, L.st, nullptr, p);
+    });
+}
+
 template <typename T>
 static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_cache &k, int layer, const void *q,
                               int B, int n_q, const float *lse, const float *in, float *out, char *ws,
@@ -250,6 +291,13 @@ static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
     const Kv4ScorePlan plan = kv4_score_plan(c, k.batch, p.n_q, k.n_prefix);
+    if (plan.rows) {
+        if (c.head_dim == 64)
+            launch_kv4_scores_rows<64>(L, p, plan.n_split);
+        else
+            launch_kv4_scores_rows<128>(L, p, plan.n_split);
+        return;
+    }
     if (plan.tc) {
         if (c.head_dim == 64)
             launch_kv4_scores_tc<64>(L, p, plan, (float *)(ws + plan.part));
