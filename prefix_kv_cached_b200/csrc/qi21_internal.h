@@ -112,7 +112,7 @@ struct Kv4Work {
 //   [items][Pp][d]) and the attention reads those.
 //   rows: few query rows; CTAs of 8 or 16 rows whose keys are split.
 struct Kv4Plan {
-    bool tc, expanded, rows, ok;
+    bool tc, expanded, rows, cluster, ok;
     int n_split;                 // rows and CUDA-core kernels: parts the keys are split into
     Kv4Work w;
     size_t err, part_l, part_o, expand, total;
@@ -136,6 +136,10 @@ constexpr int KV4_EXPAND_WAVES = 1;
 #ifndef KV4_ROWS_MAX
 #define KV4_ROWS_MAX 32
 #endif
+// Key splits that a cluster merges: the portable cluster size.
+#ifndef KV4_ROWS_CLUSTER
+#define KV4_ROWS_CLUSTER 8
+#endif
 
 inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
     Kv4Plan p{};
@@ -144,15 +148,21 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t 
     p.ok = true;
     p.tc = c.dtype == QI21_DTYPE_BF16 && tc_enabled();
     if (p.tc && n_q <= KV4_ROWS_MAX) {
-        // two CTAs an SM, at least a 64-key chunk for each of a CTA's four warps
+        // three CTAs of 8 rows or two of 16 an SM, at least a 64-key chunk for each of a
+        // CTA's four warps
         p.rows = true;
         const int64_t tile = n_q <= 8 ? 8 : 16, ctas = (n_q + tile - 1) / tile * H * B;
         const int64_t chunks = (P + 63) / 64 + (n_tail + 63) / 64;
-        int64_t n = 2 * KV4_SMS / ctas;
+        int64_t n = (tile == 8 ? 3 : 2) * KV4_SMS / ctas;
         if (n > (chunks + 3) / 4) n = (chunks + 3) / 4;
+        // merged within a cluster, without a second pass over partial results, where that
+        // costs at most an eighth of the splits (one row, 32 heads of 128, P 33792: 13
+        // splits and the pass 55 us, 8 in a cluster 66; 16 rows: 9 and the pass 66, 8 62)
+        p.cluster = n > 1 && n <= KV4_ROWS_CLUSTER + KV4_ROWS_CLUSTER / 8;
+        if (p.cluster && n > KV4_ROWS_CLUSTER) n = KV4_ROWS_CLUSTER;
         p.n_split = (int)(n < 1 ? 1 : n);
         if (B * p.n_split > 65535) p.ok = false;
-        rows = p.n_split > 1 ? (size_t)(B * H * n_q) * p.n_split : 0;
+        rows = p.n_split > 1 && !p.cluster ? (size_t)(B * H * n_q) * p.n_split : 0;
     } else if (p.tc) {
         const int64_t ur = n_q <= 128 ? 128 : 256, qt = (n_q + ur - 1) / ur, units = B * H * qt;
         const int64_t tp = (P + 127) / 128, tiles = tp + (n_tail + 127) / 128, steps = units * tiles;

@@ -101,6 +101,14 @@ __device__ __forceinline__ float kv4_code(float x, float s, float r) {
     return k;
 }
 
+// The two constants of the expansion to bf16 (kv4_pairs), as kernel parameters: from
+// there both are register or constant-bank operands and (w & mask) | one is a single
+// LOP3; as literals they are two.
+struct Kv4Lop {
+    uint32_t mask, one;          // 0x00780078, 0x41804180
+};
+constexpr Kv4Lop kKv4Lop{0x00780078u, 0x41804180u};
+
 constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row kernels handles
 
 // Quantise rows [0, P) of every (layer, K|V, item) slab of a cache in token-major
@@ -336,11 +344,12 @@ struct Kv4AttnArgs {
     int n_tail;
     void *out;                   // [B][n_q][d]
     float *lse;                  // [H][B][n_q] or null
-    int n_split;
+    int n_split, cluster;        // cluster: the splits are merged within a cluster
     float *part_l;               // [B][H][n_split][n_q]       log2-sum-exp
     float *part_o;               // [B][H][n_split][n_q][DH]
     float scale_log2;            // log2(e) / sqrt(Dh)
     uint32_t *err;
+    Kv4Lop lop;
 };
 
 constexpr float KV4_LN2 = 0.69314718055994531f;
@@ -529,17 +538,23 @@ __global__ void __launch_bounds__(256) k_kv4_combine(Kv4AttnArgs p) {
     if (row >= p.n_q) return;
     const int64_t at0 = ((int64_t)b * p.c.H + h) * p.n_split * p.n_q + row;
     float m = -INFINITY;
-    for (int s = 0; s < p.n_split; ++s) m = fmaxf(m, p.part_l[at0 + (int64_t)s * p.n_q]);
+    for (int s = lane; s < p.n_split; s += 32) m = fmaxf(m, p.part_l[at0 + (int64_t)s * p.n_q]);
+    m = warp_max(m);
     const float mz = m == -INFINITY ? 0.f : m;
     float sum = 0.f, o[DH / 32];
 #pragma unroll
     for (int j = 0; j < DH / 32; ++j) o[j] = 0.f;
-    for (int s = 0; s < p.n_split; ++s) {
-        const int64_t at = at0 + (int64_t)s * p.n_q;
-        const float w = exp2f(p.part_l[at] - mz);
-        sum += w;
+    for (int s0 = 0; s0 < p.n_split; s0 += 32) {            // 32 weights at a time, one a lane
+        const int n = min(32, p.n_split - s0);
+        const float w = lane < n ? exp2f(p.part_l[at0 + (int64_t)(s0 + lane) * p.n_q] - mz) : 0.f;
+        sum += warp_sum(w);
+#pragma unroll 8
+        for (int s = 0; s < n; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, w, s);
+            const float *src = p.part_o + (at0 + (int64_t)(s0 + s) * p.n_q) * DH + lane;
 #pragma unroll
-        for (int j = 0; j < DH / 32; ++j) o[j] = fmaf(w, p.part_o[at * DH + lane + 32 * j], o[j]);
+            for (int j = 0; j < DH / 32; ++j) o[j] = fmaf(ws, src[32 * j], o[j]);
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int d = p.c.H * DH;
@@ -567,6 +582,7 @@ struct Kv4ScoreArgs {
     float *out;                  // may be in
     float scale_log2;
     uint32_t *err;
+    Kv4Lop lop;
 };
 
 template <int DH>

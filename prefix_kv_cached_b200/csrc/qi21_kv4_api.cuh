@@ -119,9 +119,14 @@ static void launch_kv4_attn_rows(Launcher &L, const Kv4AttnArgs &p) {
     constexpr size_t smem = Kv4RowsCfg<DH, true>::SMEM;
     auto go = [&](auto *kernel, int tile, DeviceFlags &attr) {
         smem_opt_in(kernel, (int)smem, attr);
+        cudaLaunchAttribute cl;
+        cl.id = cudaLaunchAttributeClusterDimension;
+        cl.val.clusterDim.x = 1;
+        cl.val.clusterDim.y = 1;
+        cl.val.clusterDim.z = p.n_split;
         L.run("kv4_attn", [&] {
             launch_dep(kernel, dim3((p.n_q + tile - 1) / tile, p.c.H, p.B * p.n_split), dim3(32 * KV4R_WARPS), smem, L.st,
-                       nullptr, p);
+                       p.cluster ? &cl : nullptr, p);
         });
     };
     if (p.n_q <= 8) {
@@ -131,7 +136,7 @@ static void launch_kv4_attn_rows(Launcher &L, const Kv4AttnArgs &p) {
         static DeviceFlags attr;
         go(k_kv4_attn_rows<DH, 2>, 16, attr);
     }
-    if (p.n_split > 1)
+    if (p.n_split > 1 && !p.cluster)
         L.run("kv4_combine", [&] {
             launch_dep(k_kv4_combine<bf16, DH>, dim3((p.n_q + 7) / 8, p.c.H, p.B), dim3(256), 0, L.st, nullptr, p);
         });
@@ -199,10 +204,12 @@ static void launch_kv4_attention(Launcher &L, const qi21_config &c, const qi21_k
     p.out = out;
     p.lse = lse;
     p.n_split = plan.n_split;
+    p.cluster = plan.cluster;
     p.part_l = (float *)(ws + plan.part_l);
     p.part_o = (float *)(ws + plan.part_o);
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
+    p.lop = kKv4Lop;
     if (plan.rows) {
         if (c.head_dim == 64)
             launch_kv4_attn_rows<64>(L, p);
@@ -290,6 +297,7 @@ static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_
     p.out = out;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.head_dim);
     p.err = err;
+    p.lop = kKv4Lop;
     const Kv4ScorePlan plan = kv4_score_plan(c, k.batch, p.n_q, k.n_prefix);
     if (plan.rows) {
         if (c.head_dim == 64)

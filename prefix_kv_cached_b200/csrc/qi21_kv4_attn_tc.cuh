@@ -73,20 +73,29 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t s) { return s | (s << 16); }
+__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t s) {
+    uint32_t p;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(p) : "r"(s));
+    return p;
+}
 __device__ __forceinline__ uint32_t kv4_offset_pair(uint32_t s2) {   // -24 s, exact
     return fma_bf16x2(s2, 0xC1C0C1C0u, 0x80008000u);
 }
 // Nibbles i and i + 4 of w, i = 0 .. 3, as the values of a pair.
-__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t s2, uint32_t off2, uint32_t (&p)[4]) {
-    p[0] = fma_bf16x2(((w << 3) & 0x00780078u) | 0x41804180u, s2, off2);
-    p[1] = fma_bf16x2(((w >> 1) & 0x00780078u) | 0x41804180u, s2, off2);
-    p[2] = fma_bf16x2(((w >> 5) & 0x00780078u) | 0x41804180u, s2, off2);
-    p[3] = fma_bf16x2(((w >> 9) & 0x00780078u) | 0x41804180u, s2, off2);
+__device__ __forceinline__ uint32_t kv4_nibbles(uint32_t w, const Kv4Lop &k) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(k.mask), "r"(k.one));   // (w & mask) | one
+    return d;
 }
-__device__ __forceinline__ uint4 kv4_expand(uint32_t w, uint32_t s2, uint32_t off2) {
+__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k, uint32_t (&p)[4]) {
+    p[0] = fma_bf16x2(kv4_nibbles(w << 3, k), s2, off2);
+    p[1] = fma_bf16x2(kv4_nibbles(w >> 1, k), s2, off2);
+    p[2] = fma_bf16x2(kv4_nibbles(w >> 5, k), s2, off2);
+    p[3] = fma_bf16x2(kv4_nibbles(w >> 9, k), s2, off2);
+}
+__device__ __forceinline__ uint4 kv4_expand(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k) {
     uint32_t p[4];
-    kv4_pairs(w, s2, off2, p);
+    kv4_pairs(w, s2, off2, k, p);
     return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
                       __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
 }
@@ -113,7 +122,7 @@ __device__ __forceinline__ void reg_dec() {
 // swizzle.
 template <int DH, int W>
 __device__ __forceinline__ void kv4_expand_tile(uint8_t *dst, const uint8_t *codes, const uint8_t *scales, int n_rows,
-                                                int warp, int lane) {
+                                                int warp, int lane, const Kv4Lop &k) {
     constexpr int G = DH / KV4_GROUP, RPW = 32 / G, ROWS = 128 / W;     // rows of a warp at a time, and in all
     const int g = G == 4 ? (lane & 1) | ((lane >> 2) & 2) : lane & 1;
     const int r0 = G == 4 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : ((lane >> 1) & 3) | ((lane >> 3) << 2);
@@ -126,10 +135,10 @@ __device__ __forceinline__ void kv4_expand_tile(uint8_t *dst, const uint8_t *cod
         const uint32_t s2 = kv4_scale_pair(s), off2 = kv4_offset_pair(s2);
         uint8_t *row = dst + (g >> 1) * (128 * 128) + r * 128;
         const int c0 = (g & 1) * 4, x = r & 7;
-        *reinterpret_cast<uint4 *>(row + (((c0 + 0) ^ x) << 4)) = kv4_expand(w.x, s2, off2);
-        *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ x) << 4)) = kv4_expand(w.y, s2, off2);
-        *reinterpret_cast<uint4 *>(row + (((c0 + 2) ^ x) << 4)) = kv4_expand(w.z, s2, off2);
-        *reinterpret_cast<uint4 *>(row + (((c0 + 3) ^ x) << 4)) = kv4_expand(w.w, s2, off2);
+        *reinterpret_cast<uint4 *>(row + (((c0 + 0) ^ x) << 4)) = kv4_expand(w.x, s2, off2, k);
+        *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ x) << 4)) = kv4_expand(w.y, s2, off2, k);
+        *reinterpret_cast<uint4 *>(row + (((c0 + 2) ^ x) << 4)) = kv4_expand(w.z, s2, off2, k);
+        *reinterpret_cast<uint4 *>(row + (((c0 + 3) ^ x) << 4)) = kv4_expand(w.w, s2, off2, k);
     }
 }
 
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(512, 1)
                         {
                             const uint8_t *stage = smem + C::OFF_ST + ss * C::STAGE_BYTES;
                             kv4_expand_tile<DH, 4>(dst, stage, stage + C::CODE_BYTES, seg.len - tile * 128, warp - 8,
-                                                   lane);
+                                                   lane, p.a.lop);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();

@@ -2,7 +2,7 @@
 // (BF16 mode): the calls whose time is that of reading the cache once.
 //
 // A warp streams 64-key chunks of one head through a ring of its own (bulk copies,
-// three stages, no other warp to wait for) and never writes an expanded value to
+// no other warp to wait for) and never writes an expanded value to
 // memory: the codes become the register operands of mma.sync m16n8k16 with the
 // cache as the 16-row operand and 8 queries as the columns,
 //   S^T (16 keys x 8 queries)  = K Q^T   over the dims,
@@ -17,7 +17,8 @@
 //     scales; nibble i of them is row g of product tile i.
 // P^T comes from S^T by packing to bf16 and a transposing 8 x 8 move. Softmax per
 // chunk, in fp32, the running maximum per query; the warps of a CTA are merged
-// through shared memory and the key splits by k_kv4_combine, both in a fixed order.
+// through shared memory and up to KV4R_CLUSTER key splits through the shared memory of a
+// cluster (else by k_kv4_combine), in a fixed order.
 // (tcgen05 would want the expanded cache in shared memory: 2 bytes an element
 // written and read again, which alone is as long as the read of 4.5 bits from HBM.)
 // Bound by HBM; next the ALU pipe, about 1.4 operations an element at half rate.
@@ -26,27 +27,37 @@
 
 namespace qi21 {
 
-constexpr int KV4R_CHUNK = 64, KV4R_WARPS = 4, KV4R_STAGES = 3;
+constexpr int KV4R_CHUNK = 64, KV4R_WARPS = 4, KV4R_M = KV4R_CHUNK / 16;   // product tiles of keys a chunk
+constexpr int KV4R_CLUSTER = KV4_ROWS_CLUSTER;
 
 template <int DH, bool V>      // V: with the value rows
 struct Kv4RowsCfg {
     static constexpr int G = DH / KV4_GROUP;
     static constexpr int CODES = KV4R_CHUNK * DH / 2, SCALES = KV4R_CHUNK * G * 2;
     static constexpr int STAGE = (V ? 2 : 1) * (CODES + SCALES);
-    static constexpr int OFF_BAR = KV4R_WARPS * KV4R_STAGES * STAGE;
-    static constexpr size_t SMEM = (size_t)OFF_BAR + KV4R_WARPS * KV4R_STAGES * 8 + 16;
+    static constexpr int STAGES = V ? 2 : 3;
+    static constexpr int OFF_BAR = KV4R_WARPS * STAGES * STAGE;
+    static constexpr size_t SMEM = (size_t)OFF_BAR + KV4R_WARPS * STAGES * 8 + 16;
 };
 
+// ORDERED: kept in program order, which keeps the operands of later products out of
+// the registers.
+template <bool ORDERED = false>
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (ORDERED)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 
@@ -66,7 +77,7 @@ struct Kv4Ring {
     uint64_t *bars;
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;   // of the head
     __device__ __forceinline__ void load(int n, int chunk) const {           // one lane
-        const int s = n % KV4R_STAGES;
+        const int s = n % C::STAGES;
         const uint32_t dst = sm100::smem_u32(stages + s * C::STAGE), bar = sm100::smem_u32(&bars[s]);
         const int64_t r = (int64_t)chunk * KV4R_CHUNK;
         sm100::mbar_arrive_expect_tx(bar, C::STAGE);
@@ -112,49 +123,91 @@ __device__ __forceinline__ void kv4_scores_step(const uint32_t (&ka)[4], const u
     }
 }
 
-// S^T of the 16 keys from row r of a staged chunk.
-template <int DH, int NT>
+// S^T of MM tiles of 16 keys from row r of a staged chunk. The tiles take turns, so
+// that a product does not wait for the one before it.
+template <int DH, int NT, int MM, bool ORDERED = false>
 __device__ __forceinline__ void kv4_scores_staged(const uint8_t *codes, const uint8_t *scales, int r, int g, int t,
-                                                  const uint32_t (&bq)[NT][DH / 16][2], float (&s)[NT][4]) {
-    constexpr int G = DH / KV4_GROUP;
-    alignas(16) uint32_t wa[DH / 32], wb[DH / 32];
-    const uint8_t *pa = codes + (r + g) * (DH / 2) + t * (DH / 8), *pb = pa + 8 * (DH / 2);
-    if (DH == 128) {
-        *reinterpret_cast<uint4 *>(wa) = *reinterpret_cast<const uint4 *>(pa);
-        *reinterpret_cast<uint4 *>(wb) = *reinterpret_cast<const uint4 *>(pb);
-    } else {
-        *reinterpret_cast<uint2 *>(wa) = *reinterpret_cast<const uint2 *>(pa);
-        *reinterpret_cast<uint2 *>(wb) = *reinterpret_cast<const uint2 *>(pb);
-    }
+                                                  const uint32_t (&bq)[NT][DH / 16][2], const Kv4Lop &k,
+                                                  float (*s)[NT][4]) {
+    constexpr int G = DH / KV4_GROUP, W = DH / 32;
+    alignas(16) uint32_t wd[MM][2][W];             // code words of keys g and g + 8
+    uint32_t sc[MM][2], of[MM][2];
     const int grp = t * G / 4;
-    const uint32_t sa = kv4_scale_pair(*reinterpret_cast<const uint16_t *>(scales + ((r + g) * G + grp) * 2));
-    const uint32_t sb = kv4_scale_pair(*reinterpret_cast<const uint16_t *>(scales + ((r + g + 8) * G + grp) * 2));
-    const uint32_t oa = kv4_offset_pair(sa), ob = kv4_offset_pair(sb);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int m = 0; m < MM; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+            const int row = r + 16 * m + 8 * i + g;
+            const uint8_t *src = codes + row * (DH / 2) + t * (DH / 8);
+            if (DH == 128) *reinterpret_cast<uint4 *>(wd[m][i]) = *reinterpret_cast<const uint4 *>(src);
+            else *reinterpret_cast<uint2 *>(wd[m][i]) = *reinterpret_cast<const uint2 *>(src);
+            sc[m][i] = kv4_scale_pair(*reinterpret_cast<const uint16_t *>(scales + (row * G + grp) * 2));
+            of[m][i] = kv4_offset_pair(sc[m][i]);
+        }
 #pragma unroll
-    for (int w = 0; w < DH / 32; ++w) {
-        uint32_t ka[4], kb[4];
-        kv4_pairs(wa[w], sa, oa, ka);
-        kv4_pairs(wb[w], sb, ob, kb);
-        kv4_scores_step<DH, NT>(ka, kb, w, bq, s);
+    for (int m = 0; m < MM; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[m][j][i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        uint32_t ka[MM][4], kb[MM][4];
+#pragma unroll
+        for (int m = 0; m < MM; ++m) {
+            kv4_pairs(wd[m][0][w], sc[m][0], of[m][0], k, ka[m]);
+            kv4_pairs(wd[m][1][w], sc[m][1], of[m][1], k, kb[m]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int m = 0; m < MM; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    mma_bf16<ORDERED>(s[m][j], ka[m][2 * i], kb[m][2 * i], ka[m][2 * i + 1], kb[m][2 * i + 1],
+                             bq[j][2 * w + i][0], bq[j][2 * w + i][1]);
     }
 }
 
-// grid (query tiles of 8 NT rows, H, B * n_split)
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// Four finished dims of a query row from their sums, the maximum (log2 units) and the
+// sum of the weights.
+template <int DH>
+__device__ __forceinline__ void kv4_rows_store(const Kv4AttnArgs &p, int b, int h, int row, int c4, float4 o, float m,
+                                               float l) {
+    if (row >= p.n_q) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;                 // no key: 0
+    bf16 *dst = (bf16 *)p.out + ((int64_t)b * p.n_q + row) * ((int64_t)p.c.H * DH) + h * DH + c4;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (p.lse && c4 == 0)
+        p.lse[((int64_t)h * p.B + b) * p.n_q + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * KV4_LN2;
+}
+
+// grid (query tiles of 8 NT rows, H, B * n_split), clusters of n_split CTAs where p.cluster
 template <int DH, int NT>
-__global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_constant__ Kv4AttnArgs p) {
+__global__ void __launch_bounds__(32 * KV4R_WARPS, NT == 1 ? 3 : 2) k_kv4_attn_rows(const __grid_constant__ Kv4AttnArgs p) {
     using namespace sm100;
     using C = Kv4RowsCfg<DH, true>;
     constexpr int MT = DH / 16;                    // product tiles of 16 dims
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + KV4R_WARPS * KV4R_STAGES);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + KV4R_WARPS * C::STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < KV4R_WARPS * KV4R_STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
+        for (int i = 0; i < KV4R_WARPS * C::STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -172,15 +225,15 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
     const int n_all = first < hi ? (hi - first + KV4R_WARPS - 1) / KV4R_WARPS : 0;
     const int n_pre = first < min(hi, cp) ? (min(hi, cp) - first + KV4R_WARPS - 1) / KV4R_WARPS : 0;
     Kv4Ring<DH, true> ring;
-    ring.stages = smem + warp * KV4R_STAGES * C::STAGE;
-    ring.bars = bars + warp * KV4R_STAGES;
+    ring.stages = smem + warp * C::STAGES * C::STAGE;
+    ring.bars = bars + warp * C::STAGES;
     const int64_t kr = kv4_row0(p.c, p.layer, 0, cb, h), vr = kv4_row0(p.c, p.layer, 1, cb, h);
     ring.k_codes = p.base + kr * (DH / 2);
     ring.v_codes = p.base + vr * (DH / 2);
     ring.k_scales = p.base + p.c.scales_off + kr * (C::G * 2);
     ring.v_scales = p.base + p.c.scales_off + vr * (C::G * 2);
     if (lane == 0)
-        for (int n = 0; n < min(n_pre, KV4R_STAGES); ++n) ring.load(n, first + n * KV4R_WARPS);
+        for (int n = 0; n < min(n_pre, C::STAGES); ++n) ring.load(n, first + n * KV4R_WARPS);
     uint32_t bq[NT][DH / 16][2];
     kv4_load_q<DH, NT>((const bf16 *)p.q + (int64_t)b * p.n_q * d + h * DH, q0, p.n_q, d, g, t, bq);
     const bf16 *kt = (const bf16 *)p.k_tail + (int64_t)b * p.n_tail * d + h * DH;
@@ -202,18 +255,20 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
         const int chunk = first + n * KV4R_WARPS;
         const bool pre = n < n_pre;
         const int n_keys = pre ? len - chunk * KV4R_CHUNK : p.n_tail - (chunk - cp) * KV4R_CHUNK;
-        const uint8_t *st = ring.stages + (n % KV4R_STAGES) * C::STAGE;
+        const uint8_t *st = ring.stages + (n % C::STAGES) * C::STAGE;
         const bf16 *kc = kt + (int64_t)(chunk - cp) * KV4R_CHUNK * d, *vc = vt + (int64_t)(chunk - cp) * KV4R_CHUNK * d;
         if (pre) {
-            const bool ok = mbar_wait(smem_u32(&ring.bars[n % KV4R_STAGES]), (n / KV4R_STAGES) & 1, abort_flag, p.err);
+            const bool ok = mbar_wait(smem_u32(&ring.bars[n % C::STAGES]), (n / C::STAGES) & 1, abort_flag, p.err);
             if (!__all_sync(0xffffffffu, ok ? 1 : 0)) break;
         }
-        float s[4][NT][4];
+        float s[KV4R_M][NT][4];
+        if (pre) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            if (pre) {
-                kv4_scores_staged<DH, NT>(st, st + C::CODES, 16 * m, g, t, bq, s[m]);
-            } else {
+            for (int m = 0; m < KV4R_M; m += 2)
+                kv4_scores_staged<DH, NT, 2>(st, st + C::CODES, 16 * m, g, t, bq, p.lop, s + m);
+        } else {
+#pragma unroll
+            for (int m = 0; m < KV4R_M; ++m) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -232,48 +287,59 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
             }
         }
         // softmax of the chunk: scores of keys 16 m + g (values 0, 1) and 16 m + 8 + g (2, 3)
-        float alpha[NT][2];
+        const bool partial = n_keys < KV4R_CHUNK;
+        if (partial) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float mx[2] = {-INFINITY, -INFINITY};
+            for (int m = 0; m < KV4R_M; ++m)
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool live = 16 * m + g + (i >> 1) * 8 < n_keys;
-                    s[m][j][i] = live ? s[m][j][i] * p.scale_log2 : -INFINITY;
-                    mx[i & 1] = fmaxf(mx[i & 1], s[m][j][i]);
-                }
+                    for (int i = 0; i < 4; ++i)
+                        if (16 * m + g + (i >> 1) * 8 >= n_keys) s[m][j][i] = -INFINITY;
+        }
+        bool moved = false;
+        float alpha[NT][2], mc[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                float mx = mr[j][i];
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
-                const float mn = fmaxf(mr[j][i], mx[i]), mz = mn == -INFINITY ? 0.f : mn;
-                alpha[j][i] = ex2_approx(mr[j][i] - mz);
-                mr[j][i] = mn;
-                lr[j][i] *= alpha[j][i];
-                mx[i] = mz;
+                for (int m = 0; m < KV4R_M; ++m) mx = fmax3(mx, s[m][j][i], s[m][j][i + 2]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                mc[j][i] = mx == -INFINITY ? 0.f : mx * p.scale_log2;
+                alpha[j][i] = ex2_approx(fmaf(mr[j][i], p.scale_log2, -mc[j][i]));
+                moved |= mx != mr[j][i];
+                mr[j][i] = mx;
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+        for (int j = 0; j < NT; ++j) {
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < KV4R_M; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    s[m][j][i] = ex2_approx(s[m][j][i] - mx[i & 1]);
-                    lr[j][i & 1] += s[m][j][i];
+                    s[m][j][i] = ex2_approx(fmaf(s[m][j][i], p.scale_log2, -mc[j][i & 1]));
+                    sum[i & 1] += s[m][j][i];
+                }
+            lr[j][0] = fmaf(lr[j][0], alpha[j][0], sum[0]);
+            lr[j][1] = fmaf(lr[j][1], alpha[j][1], sum[1]);
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[m][j][0] *= alpha[j][0];
+                    o[m][j][1] *= alpha[j][1];
+                    o[m][j][2] *= alpha[j][0];
+                    o[m][j][3] *= alpha[j][1];
                 }
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                o[m][j][0] *= alpha[j][0];
-                o[m][j][1] *= alpha[j][1];
-                o[m][j][2] *= alpha[j][0];
-                o[m][j][3] *= alpha[j][1];
-            }
         // O^T += V^T P^T, 16 keys at a time
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < KV4R_M; ++m) {
             uint32_t bp[NT][2];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -289,34 +355,36 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
                     const int grp = g * C::G / 8;
                     uint32_t s0 = *reinterpret_cast<const uint16_t *>(vscales + (k0 * C::G + grp) * 2);
                     uint32_t s1 = *reinterpret_cast<const uint16_t *>(vscales + ((k0 + 1) * C::G + grp) * 2);
-                    if (k0 >= n_keys) s0 = 0;                  // what those rows hold stays out
-                    if (k0 + 1 >= n_keys) s1 = 0;
-                    const uint32_t s2 = s0 | (s1 << 16), o2 = kv4_offset_pair(s2);
+                    if (partial) {                             // what rows that do not exist hold stays out
+                        if (k0 >= n_keys) s0 = 0;
+                        if (k0 + 1 >= n_keys) s1 = 0;
+                    }
+                    const uint32_t s2 = __byte_perm(s0, s1, 0x5410), o2 = kv4_offset_pair(s2);
                     const uint8_t *pv = vcodes + k0 * (DH / 2) + g * (DH / 16);
                     if (DH == 128) {
                         const uint2 w0 = *reinterpret_cast<const uint2 *>(pv);
                         const uint2 w1 = *reinterpret_cast<const uint2 *>(pv + DH / 2);
                         uint32_t x[4];
-                        kv4_pairs(__byte_perm(w0.x, w1.x, 0x5410), s2, o2, x);
+                        kv4_pairs(__byte_perm(w0.x, w1.x, 0x5410), s2, o2, p.lop, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) a[2 * half][i] = x[i];
-                        kv4_pairs(__byte_perm(w0.x, w1.x, 0x7632), s2, o2, x);
+                        kv4_pairs(__byte_perm(w0.x, w1.x, 0x7632), s2, o2, p.lop, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) a[2 * half][(MT - 4) + i] = x[i];
-                        kv4_pairs(__byte_perm(w0.y, w1.y, 0x5410), s2, o2, x);
+                        kv4_pairs(__byte_perm(w0.y, w1.y, 0x5410), s2, o2, p.lop, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) a[2 * half + 1][i] = x[i];
-                        kv4_pairs(__byte_perm(w0.y, w1.y, 0x7632), s2, o2, x);
+                        kv4_pairs(__byte_perm(w0.y, w1.y, 0x7632), s2, o2, p.lop, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) a[2 * half + 1][(MT - 4) + i] = x[i];
                     } else {
                         const uint32_t w0 = *reinterpret_cast<const uint32_t *>(pv);
                         const uint32_t w1 = *reinterpret_cast<const uint32_t *>(pv + DH / 2);
                         uint32_t x[4];
-                        kv4_pairs(__byte_perm(w0, w1, 0x5410), s2, o2, x);
+                        kv4_pairs(__byte_perm(w0, w1, 0x5410), s2, o2, p.lop, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) a[2 * half][i] = x[i];
-                        kv4_pairs(__byte_perm(w0, w1, 0x7632), s2, o2, x);
+                        kv4_pairs(__byte_perm(w0, w1, 0x7632), s2, o2, p.lop, x);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) a[2 * half + 1][i] = x[i];
                     }
@@ -347,7 +415,7 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
                 for (int j = 0; j < NT; ++j) mma_bf16(o[i][j], a[0][i], a[1][i], a[2][i], a[3][i], bp[j][0], bp[j][1]);
         }
         __syncwarp();
-        if (pre && lane == 0 && n + KV4R_STAGES < n_pre) ring.load(n + KV4R_STAGES, chunk + KV4R_STAGES * KV4R_WARPS);
+        if (pre && lane == 0 && n + C::STAGES < n_pre) ring.load(n + C::STAGES, chunk + C::STAGES * KV4R_WARPS);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -364,7 +432,7 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                st_m[(warp * 2 + 0) * 8 * NT + 8 * j + 2 * t + i] = mr[j][i];
+                st_m[(warp * 2 + 0) * 8 * NT + 8 * j + 2 * t + i] = mr[j][i] * p.scale_log2;
                 st_m[(warp * 2 + 1) * 8 * NT + 8 * j + 2 * t + i] = lr[j][i];
             }
     }
@@ -379,38 +447,91 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
                 st_o[(warp * 8 * NT + 8 * j + 2 * t + (i & 1)) * DH + dim] = o[m][j][i];
             }
     __syncthreads();
-    for (int e = threadIdx.x; e < 8 * NT * (DH / 4); e += 32 * KV4R_WARPS) {
-        const int r = e / (DH / 4), c4 = (e - r * (DH / 4)) * 4, row = q0 + r;
-        if (row >= p.n_q) continue;
+    // the CTA's own result, not normalised: a thread keeps its elements of it
+    constexpr int ELEMS = 8 * NT * (DH / 4), PER = (ELEMS + 32 * KV4R_WARPS - 1) / (32 * KV4R_WARPS);
+    float4 acc[PER];
+    float am[PER], al[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x + i * 32 * KV4R_WARPS, r = e / (DH / 4), c4 = (e - r * (DH / 4)) * 4;
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < KV4R_WARPS; ++w) m = fmaxf(m, st_m[w * 2 * 8 * NT + r]);
         const float mz = m == -INFINITY ? 0.f : m;
         float l = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < KV4R_WARPS; ++w) {
             const float f = ex2_approx(st_m[w * 2 * 8 * NT + r] - mz);
             l = fmaf(f, st_m[(w * 2 + 1) * 8 * NT + r], l);
             const float4 v = *reinterpret_cast<const float4 *>(st_o + (w * 8 * NT + r) * DH + c4);
-            a.x = fmaf(f, v.x, a.x);
-            a.y = fmaf(f, v.y, a.y);
-            a.z = fmaf(f, v.z, a.z);
-            a.w = fmaf(f, v.w, a.w);
+            v4.x = fmaf(f, v.x, v4.x);
+            v4.y = fmaf(f, v.y, v4.y);
+            v4.z = fmaf(f, v.z, v4.z);
+            v4.w = fmaf(f, v.w, v4.w);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? -INFINITY : mz + log2f(l);
-        a.x *= inv;
-        a.y *= inv;
-        a.z *= inv;
-        a.w *= inv;
+        acc[i] = v4;
+        am[i] = m;
+        al[i] = l;
+    }
+    if (p.cluster) {
+        // the splits are the CTAs of a cluster: every one publishes its result and
+        // finishes a share of the elements from all of them
+        __syncthreads();
+        float *cl = reinterpret_cast<float *>(smem);            // [ELEMS] x (4 outputs, m, l)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + i * 32 * KV4R_WARPS;
+            if (e < ELEMS) {
+                reinterpret_cast<float4 *>(cl)[e] = acc[i];
+                reinterpret_cast<float2 *>(cl + 4 * ELEMS)[e] = make_float2(am[i], al[i]);
+            }
+        }
+        cluster_sync();
+        const uint32_t base = smem_u32(cl);
+        for (int e = sp * 32 * KV4R_WARPS + threadIdx.x; e < ELEMS; e += p.n_split * 32 * KV4R_WARPS) {
+            float m = -INFINITY;
+            float2 ml[KV4R_CLUSTER];
+            float4 v[KV4R_CLUSTER];
+#pragma unroll
+            for (int w = 0; w < KV4R_CLUSTER; ++w) {
+                ml[w] = make_float2(-INFINITY, 0.f);
+                v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (w < p.n_split) {
+                    ml[w] = ld_cluster_f2(mapa_shared(base + 16 * ELEMS + 8 * e, w));
+                    v[w] = ld_cluster_f4(mapa_shared(base + 16 * e, w));
+                    m = fmaxf(m, ml[w].x);
+                }
+            }
+            const float mz = m == -INFINITY ? 0.f : m;
+            float l = 0.f;
+            float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < KV4R_CLUSTER; ++w) {
+                const float f = ex2_approx(ml[w].x - mz);
+                l = fmaf(f, ml[w].y, l);
+                o4.x = fmaf(f, v[w].x, o4.x);
+                o4.y = fmaf(f, v[w].y, o4.y);
+                o4.z = fmaf(f, v[w].z, o4.z);
+                o4.w = fmaf(f, v[w].w, o4.w);
+            }
+            kv4_rows_store<DH>(p, b, h, q0 + e / (DH / 4), (e % (DH / 4)) * 4, o4, m, l);
+        }
+        cluster_sync();                                        // nobody leaves while it is read
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x + i * 32 * KV4R_WARPS, r = e / (DH / 4), c4 = (e - r * (DH / 4)) * 4, row = q0 + r;
+        if (e >= ELEMS || row >= p.n_q) continue;
         if (p.n_split == 1) {
-            bf16 *dst = (bf16 *)p.out + ((int64_t)b * p.n_q + row) * d + h * DH + c4;
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-            if (p.lse && c4 == 0) p.lse[((int64_t)h * p.B + b) * p.n_q + row] = lse2 * KV4_LN2;
+            kv4_rows_store<DH>(p, b, h, row, c4, acc[i], am[i], al[i]);
         } else {
+            const float inv = al[i] == 0.f ? 0.f : 1.f / al[i];
             const int64_t at = (((int64_t)b * p.c.H + h) * p.n_split + sp) * p.n_q + row;
-            *reinterpret_cast<float4 *>(p.part_o + at * DH + c4) = a;
-            if (c4 == 0) p.part_l[at] = lse2;
+            *reinterpret_cast<float4 *>(p.part_o + at * DH + c4) =
+                make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+            if (c4 == 0) p.part_l[at] = al[i] == 0.f ? -INFINITY : am[i] + log2f(al[i]);
         }
     }
 }
@@ -419,15 +540,15 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_attn_rows(const __grid_
 // 8 NT over the staged chunk. grid (key splits, H, cache items); a split's warps take
 // its chunks in turn, and every key's sum is one warp's.
 template <int DH>
-__global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_scores_rows(const __grid_constant__ Kv4ScoreArgs p) {
+__global__ void __launch_bounds__(32 * KV4R_WARPS, 4) k_kv4_scores_rows(const __grid_constant__ Kv4ScoreArgs p) {
     using namespace sm100;
     using C = Kv4RowsCfg<DH, false>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + KV4R_WARPS * KV4R_STAGES);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + KV4R_WARPS * C::STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < KV4R_WARPS * KV4R_STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
+        for (int i = 0; i < KV4R_WARPS * C::STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -446,14 +567,14 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_scores_rows(const __gri
     const int end = min(hi, (len + KV4R_CHUNK - 1) / KV4R_CHUNK);
     const int n_pre = first < end ? (end - first + KV4R_WARPS - 1) / KV4R_WARPS : 0;
     Kv4Ring<DH, false> ring;
-    ring.stages = smem + warp * KV4R_STAGES * C::STAGE;
-    ring.bars = bars + warp * KV4R_STAGES;
+    ring.stages = smem + warp * C::STAGES * C::STAGE;
+    ring.bars = bars + warp * C::STAGES;
     const int64_t kr = kv4_row0(p.c, p.layer, 0, b, h);
     ring.k_codes = p.base + kr * (DH / 2);
     ring.k_scales = p.base + p.c.scales_off + kr * (C::G * 2);
     ring.v_codes = ring.v_scales = nullptr;
     if (lane == 0)
-        for (int n = 0; n < min(n_pre, KV4R_STAGES); ++n) ring.load(n, first + n * KV4R_WARPS);
+        for (int n = 0; n < min(n_pre, C::STAGES); ++n) ring.load(n, first + n * KV4R_WARPS);
     const bf16 *q = (const bf16 *)p.q + (int64_t)b * p.n_q * d + h * DH;
     const float *lse = p.lse + ((int64_t)h * p.c.B + b) * p.n_q;
     uint32_t bq[1][DH / 16][2];
@@ -466,28 +587,30 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS) k_kv4_scores_rows(const __gri
     fetch(0);
     for (int n = 0; n < n_all; ++n) {
         const int chunk = first + n * KV4R_WARPS, n_keys = n < n_pre ? len - chunk * KV4R_CHUNK : 0;
-        float sum[4][2];                               // keys 16 m + g and 16 m + 8 + g
+        float sum[KV4R_M][2];                               // keys 16 m + g and 16 m + 8 + g
 #pragma unroll
-        for (int m = 0; m < 4; ++m) sum[m][0] = sum[m][1] = 0.f;
+        for (int m = 0; m < KV4R_M; ++m) sum[m][0] = sum[m][1] = 0.f;
         if (n < n_pre) {
-            const uint8_t *st = ring.stages + (n % KV4R_STAGES) * C::STAGE;
-            const bool ok = mbar_wait(smem_u32(&ring.bars[n % KV4R_STAGES]), (n / KV4R_STAGES) & 1, abort_flag, p.err);
+            const uint8_t *st = ring.stages + (n % C::STAGES) * C::STAGE;
+            const bool ok = mbar_wait(smem_u32(&ring.bars[n % C::STAGES]), (n / C::STAGES) & 1, abort_flag, p.err);
             if (!__all_sync(0xffffffffu, ok ? 1 : 0)) break;
             for (int q0 = 0; q0 < p.n_q; q0 += 8) {
                 if (p.n_q > 8) fetch(q0);
+                float s[KV4R_M][1][4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    float s[1][4];
-                    kv4_scores_staged<DH, 1>(st, st + C::CODES, 16 * m, g, t, bq, s);
+                for (int m = 0; m < KV4R_M; ++m)
+                    kv4_scores_staged<DH, 1, 1, true>(st, st + C::CODES, 16 * m, g, t, bq, p.lop, s + m);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[m][i >> 1] += ex2_approx(fmaf(s[0][i], p.scale_log2, off[i & 1]));
-                }
+                for (int m = 0; m < KV4R_M; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sum[m][i >> 1] += ex2_approx(fmaf(s[m][0][i], p.scale_log2, off[i & 1]));
             }
             __syncwarp();
-            if (lane == 0 && n + KV4R_STAGES < n_pre) ring.load(n + KV4R_STAGES, chunk + KV4R_STAGES * KV4R_WARPS);
+            if (lane == 0 && n + C::STAGES < n_pre) ring.load(n + C::STAGES, chunk + C::STAGES * KV4R_WARPS);
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < KV4R_M; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float a = sum[m][i];

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(320, 2)
         if (nt > 0) {
             const int64_t row = kv4_row0(p.a.c, p.a.layer, 0, b, h) + k0;
             kv4_expand_tile<DH, 8>(smem + C::OFF_K, p.a.base + row * (DH / 2),
-                                   p.a.base + p.a.c.scales_off + row * (C::G * 2), len - k0, warp, lane);
+                                   p.a.base + p.a.c.scales_off + row * (C::G * 2), len - k0, warp, lane, p.a.lop);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(k_ready));
             const uint32_t t_s = tmem_base + ((uint32_t)(quad * 32) << 16) + half * 64;
