@@ -43,6 +43,48 @@ __device__ __forceinline__ int kv4_len(const Kv4Dims &c, const int *prefix_len, 
     return n < 0 ? 0 : (n > c.P ? c.P : n);
 }
 
+// ------------------------------------------------------------------ expanding codes
+// The two constants of the expansion to bf16 (kv4_pairs), as kernel parameters: from
+// there both are register or constant-bank operands and (w & mask) | one is a single
+// LOP3; as literals they are two.
+struct Kv4Lop {
+    uint32_t mask, one;          // 0x00780078, 0x41804180
+};
+constexpr Kv4Lop kKv4Lop{0x00780078u, 0x41804180u};
+
+// (nibble - 8) s of the 8 nibbles of a code word as bf16 pairs in the order of dims.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t s) {
+    uint32_t p;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(p) : "r"(s));
+    return p;
+}
+__device__ __forceinline__ uint32_t kv4_offset_pair(uint32_t s2) {   // -24 s, exact
+    return fma_bf16x2(s2, 0xC1C0C1C0u, 0x80008000u);
+}
+// Nibbles i and i + 4 of w, i = 0 .. 3, as the values of a pair.
+__device__ __forceinline__ uint32_t kv4_nibbles(uint32_t w, const Kv4Lop &k) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(k.mask), "r"(k.one));   // (w & mask) | one
+    return d;
+}
+__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k, uint32_t (&p)[4]) {
+    p[0] = fma_bf16x2(kv4_nibbles(w << 3, k), s2, off2);
+    p[1] = fma_bf16x2(kv4_nibbles(w >> 1, k), s2, off2);
+    p[2] = fma_bf16x2(kv4_nibbles(w >> 5, k), s2, off2);
+    p[3] = fma_bf16x2(kv4_nibbles(w >> 9, k), s2, off2);
+}
+__device__ __forceinline__ uint4 kv4_expand(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k) {
+    uint32_t p[4];
+    kv4_pairs(w, s2, off2, k, p);
+    return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                      __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+}
+
 // ------------------------------------------------------------------ quantise
 // 8 consecutive elements of a row as floats.
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
@@ -63,13 +105,6 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ void store8(bf16 *p, const float (&x)[8]) {   // exact: every value has 8 bits
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // The scale of a group whose largest magnitude has these bits (finite or not).
 // The candidate cuts a/7 (a product with the rounded 1/7, within 2^-23 of it) to
@@ -86,28 +121,46 @@ __device__ __forceinline__ float kv4_scale(uint32_t amax_bits) {
     return fminf(s, hi);
 }
 
-// rint(x / s) in [-7, 7], ties to even, for s > 0 with r = fl(1 / s). t = x r is
-// within 2^-22 |t| of the quotient: where it lies near the middle of two integers
-// the exact remainder x - k s decides (k s has 8 bits, and the difference is
-// exact there: Sterbenz, or k = 0).
-__device__ __forceinline__ float kv4_code(float x, float s, float r) {
-    const float t = fminf(fmaxf(x * r, -7.f), 7.f);
-    float k = rintf(t);
-    if (fabsf(t - k) > 0.4999f) {
-        const float e = fmaf(-k, s, x), e2 = 2.f * fabsf(e);
-        if (e2 > s || (e2 == s && ((int)k & 1))) k += copysignf(1.f, e);
-        k = fminf(fmaxf(k, -7.f), 7.f);
+// The code word of 8 elements of a group with scale s > 0: rint(x / s), ties to even,
+// in [-7, 7], plus 8. With r = 1 / s (within 2^-22) and M = 1.5 2^23 + 8 the two sums
+// x r (1 + 2^-20) + M and x r (1 - 2^-20) + M, each rounded once, hold integers k+ + 8
+// and k- + 8 in their low bits; where they are equal, that is the nearest integer to
+// the quotient, which lies between them. Their own sum has a unit of 2, so that it is
+// rounded to the even one of k+ and k- where these differ: the tie rule. For bf16
+// elements they differ at ties alone (8 bits over 5: a quotient that is not a half
+// integer is at least 1/1984 away from one). Elements of 24 bits can be nearer; there
+// the remainder x - k s decides, which is exact (k s has 8 bits, and the difference
+// is x itself or exact by Sterbenz' lemma).
+template <bool EXACT>
+__device__ __forceinline__ uint32_t kv4_code_word(const float (&x)[8], float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const float up = r * (1.f + 0x1p-20f), dn = r * (1.f - 0x1p-20f), M = 12582920.f;
+    uint32_t b[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float a = fmaf(x[k], up, M), c = fmaf(x[k], dn, M);
+        b[k] = __float_as_uint(a + c);
+        if (EXACT && a != c) {
+            float q = fminf(a, c) - M;                 // the lower of the two integers
+            const float e = fmaf(-q, s, x[k]), h = 0.5f * s;
+            if (e > h || (e == h && ((int)q & 1))) q += 1.f;
+            b[k] = __float_as_uint(2.f * (q + M));
+        }
     }
-    return k;
+    // the low bytes hold the codes: even ones, and odd ones a nibble further
+    const uint32_t e = __byte_perm(__byte_perm(b[0], b[2], 0x0040), __byte_perm(b[4], b[6], 0x0040), 0x5410);
+    const uint32_t o = __byte_perm(__byte_perm(b[1], b[3], 0x0040), __byte_perm(b[5], b[7], 0x0040), 0x5410);
+    return e + 16u * o;
 }
 
-// The two constants of the expansion to bf16 (kv4_pairs), as kernel parameters: from
-// there both are register or constant-bank operands and (w & mask) | one is a single
-// LOP3; as literals they are two.
-struct Kv4Lop {
-    uint32_t mask, one;          // 0x00780078, 0x41804180
-};
-constexpr Kv4Lop kKv4Lop{0x00780078u, 0x41804180u};
+// Bits of the largest magnitude of 8 consecutive elements (a NaN's lie above all others).
+__device__ __forceinline__ uint32_t kv4_max8(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+    return m;
+}
 
 constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row kernels handles
 
@@ -120,51 +173,64 @@ constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row 
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv4_quantize(const T *__restrict__ src, int64_t slab_stride, Kv4Dims c,
                                                       const int *__restrict__ prefix_len, uint8_t *__restrict__ base) {
-    const int d = c.H * c.Dh, cols = d / 8;
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint32_t d = c.H * c.Dh, cols = d / 8, u = blockIdx.x * 256 + threadIdx.x;
     const int slab = blockIdx.y;                 // (l * 2 + which) * B + b
     const int rows = kv4_len(c, prefix_len, slab % c.B);
-    const int64_t quad = u / cols;
-    const int col = (int)(u - quad * cols);      // the 4 threads of a group are lanes of one warp: cols % 4 == 0
-    const int h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
+    const uint32_t quad = u / cols, col = u - quad * cols;   // the 4 threads of a group share a warp: cols % 4 == 0
+    const uint32_t h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
+    const int64_t r0 = (int64_t)quad * KV4_Q_ROWS;
+    const T *from = src + slab * slab_stride + r0 * d + col * 8;
     float x[KV4_Q_ROWS][8];
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        const int64_t r = quad * KV4_Q_ROWS + i;
-        if (r < rows) {
-            load8(src + slab * slab_stride + r * d + col * 8, x[i]);
+        if (r0 + i < rows) {
+            load8(from + (int64_t)i * d, x[i]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
         }
     }
-    const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp;
+    const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp + r0;
+    uint8_t *codes = base + row0 * (c.Dh / 2) + j0 / 2;
+    uint16_t *scales = reinterpret_cast<uint16_t *>(base + c.scales_off) + row0 * (c.Dh / KV4_GROUP) + j0 / KV4_GROUP;
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[i][k]) & 0x7FFFFFFFu);
+        uint32_t m = kv4_max8(x[i]);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float s = kv4_scale(m), r = s > 0.f ? 1.f / s : 0.f;
-        uint32_t w = 0;
+        const float s = kv4_scale(m);
+        if (m > 0x7DE00000u) {                               // beyond 7 * 2^122: saturate
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float q = s > 0.f ? kv4_code(x[i][k], s, r) : 0.f;
-            w |= (uint32_t)((int)q + 8) << (4 * k);
+            for (int k = 0; k < 8; ++k) x[i][k] = fminf(fmaxf(x[i][k], -7.f * s), 7.f * s);
         }
-        const int64_t row = quad * KV4_Q_ROWS + i;
-        if (row < rows) {
-            *reinterpret_cast<uint32_t *>(base + (row0 + row) * (c.Dh / 2) + j0 / 2) = w;
-            if ((col & 3) == 0)
-                reinterpret_cast<uint16_t *>(base + c.scales_off)[(row0 + row) * (c.Dh / KV4_GROUP) + j0 / KV4_GROUP] =
-                    (uint16_t)(__float_as_uint(s) >> 16);
+        const uint32_t w = s > 0.f ? kv4_code_word<sizeof(T) == 4>(x[i], s) : 0x88888888u;
+        if (r0 + i < rows) {
+            *reinterpret_cast<uint32_t *>(codes + (int64_t)i * (c.Dh / 2)) = w;
+            if ((col & 3) == 0) scales[(int64_t)i * (c.Dh / KV4_GROUP)] = (uint16_t)(__float_as_uint(s) >> 16);
         }
     }
 }
 
 // ------------------------------------------------------------------ dequantise
-// The 8 values of a code word.
+// The 8 values of a code word in each storage type.
+__device__ __forceinline__ void kv4_store8(bf16 *p, uint32_t w, uint32_t s, const Kv4Lop &k) {
+    const uint32_t s2 = kv4_scale_pair(s);
+    *reinterpret_cast<uint4 *>(p) = kv4_expand(w, s2, kv4_offset_pair(s2), k);
+}
+__device__ __forceinline__ void kv4_store8(float *p, uint32_t w, uint32_t s, const Kv4Lop &k) {
+    const uint32_t s2 = kv4_scale_pair(s);
+    const uint4 v = kv4_expand(w, s2, kv4_offset_pair(s2), k);
+    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(e[i] << 16);
+        x[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+    }
+    store8(p, x);
+}
 __device__ __forceinline__ void kv4_values(uint32_t w, float s, float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = (float)((int)((w >> (4 * k)) & 15u) - 8) * s;
@@ -180,39 +246,32 @@ __device__ __forceinline__ float kv4_load_scale(const uint8_t *base, const Kv4Di
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *__restrict__ base, Kv4Dims c, int slab0,
                                                         const int *__restrict__ prefix_len, int pad,
-                                                        T *__restrict__ dst, int64_t slab_stride) {
+                                                        T *__restrict__ dst, int64_t slab_stride, Kv4Lop lop) {
     pdl_launch_dependents();
     pdl_wait();
-    const int d = c.H * c.Dh, cols = d / 8;
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t d = c.H * c.Dh, cols = d / 8, u = blockIdx.x * 256 + threadIdx.x;
     const int slab = slab0 + blockIdx.y;
     const int rows = kv4_len(c, prefix_len, slab % c.B);
-    const int64_t quad = u / cols;
-    const int col = (int)(u - quad * cols);
-    const int h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
-    const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp;
-    const int rows_out = pad ? (int)kv4_pad(rows) : rows;
-    uint32_t w[KV4_Q_ROWS];
-    float s[KV4_Q_ROWS];
+    const uint32_t quad = u / cols, col = u - quad * cols;
+    const uint32_t h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
+    const int64_t r0 = (int64_t)quad * KV4_Q_ROWS, row0 = ((int64_t)slab * c.H + h) * c.Pp + r0;
+    const uint8_t *codes = base + row0 * (c.Dh / 2) + j0 / 2;
+    const uint16_t *scales =
+        reinterpret_cast<const uint16_t *>(base + c.scales_off) + row0 * (c.Dh / KV4_GROUP) + j0 / KV4_GROUP;
+    const int64_t rows_out = pad ? kv4_pad(rows) : rows;
+    uint32_t w[KV4_Q_ROWS], s[KV4_Q_ROWS];
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        const int64_t r = quad * KV4_Q_ROWS + i;
-        w[i] = 0;
-        s[i] = 0.f;
-        if (r < rows) {
-            w[i] = *reinterpret_cast<const uint32_t *>(base + (row0 + r) * (c.Dh / 2) + j0 / 2);
-            s[i] = kv4_load_scale(base, c, row0 + r, j0 / KV4_GROUP);
+        w[i] = s[i] = 0;                         // the value 0
+        if (r0 + i < rows) {
+            w[i] = *reinterpret_cast<const uint32_t *>(codes + (int64_t)i * (c.Dh / 2));
+            s[i] = scales[(int64_t)i * (c.Dh / KV4_GROUP)];
         }
     }
+    T *to = dst + (int64_t)blockIdx.y * slab_stride + r0 * d + col * 8;
 #pragma unroll
-    for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        const int64_t r = quad * KV4_Q_ROWS + i;
-        if (r < rows_out) {
-            float x[8];
-            kv4_values(w[i], s[i], x);
-            store8(dst + (int64_t)blockIdx.y * slab_stride + r * d + col * 8, x);
-        }
-    }
+    for (int i = 0; i < KV4_Q_ROWS; ++i)
+        if (r0 + i < rows_out) kv4_store8(to + (int64_t)i * d, w[i], s[i], lop);
 }
 
 // ------------------------------------------------------------------ eviction

@@ -27,6 +27,8 @@ static qi21_status check_kv4(const qi21_config *c, const qi21_kv4_cache *k) {
         k->n_prefix <= 0 || k->n_prefix > INT32_MAX - 128)
         return QI21_ERR_CACHE_STATE;
     if ((int64_t)k->n_layers * 2 * k->batch > 65535 || k->n_heads > 65535) return QI21_ERR_SHAPE;
+    // a slab's units of 8 dims by 4 rows are counted in 32 bits
+    if (((int64_t)k->n_prefix + 131) / 4 * (c->d_model / 8) > UINT32_MAX - 256ll) return QI21_ERR_SHAPE;
     return QI21_OK;
 }
 
@@ -50,8 +52,8 @@ template <typename T>
 static void launch_kv4_quantize(Launcher &L, const qi21_config &c, const qi21_kv_cache &src,
                                 const qi21_kv4_cache &dst) {
     L.run("kv4_quantize", [&] {
-        k_kv4_quantize<T><<<kv4_row_grid(c, dst), 256, 0, L.st>>>((const T *)src.base, kv_slab_rows(src) * c.d_model,
-                                                                  kv4_dims(dst), dst.prefix_len, (uint8_t *)dst.base);
+        launch_dep(k_kv4_quantize<T>, kv4_row_grid(c, dst), dim3(256), 0, L.st, nullptr, (const T *)src.base,
+                   kv_slab_rows(src) * c.d_model, kv4_dims(dst), dst.prefix_len, (uint8_t *)dst.base);
     });
 }
 
@@ -60,7 +62,7 @@ static void launch_kv4_dequantize(Launcher &L, const qi21_config &c, const qi21_
                                   const qi21_kv_cache &dst) {
     L.run("kv4_dequantize", [&] {
         launch_dep(k_kv4_dequantize<T>, kv4_row_grid(c, src), dim3(256), 0, L.st, nullptr, (const uint8_t *)src.base,
-                   kv4_dims(src), 0, src.prefix_len, 0, (T *)dst.base, kv_slab_rows(dst) * c.d_model);
+                   kv4_dims(src), 0, src.prefix_len, 0, (T *)dst.base, kv_slab_rows(dst) * c.d_model, kKv4Lop);
     });
 }
 
@@ -151,7 +153,7 @@ static void launch_kv4_attn_expanded(Launcher &L, const Kv4AttnArgs &a, const Kv
     const int64_t quads = pp / KV4_Q_ROWS;
     L.run("kv4_expand", [&] {
         launch_dep(k_kv4_dequantize<bf16>, dim3((unsigned)((quads * (d / 8) + 255) / 256), 2 * a.c.B), dim3(256), 0,
-                   L.st, nullptr, a.base, a.c, a.layer * 2 * a.c.B, a.prefix_len, 1, ek, (int64_t)(pp * d));
+                   L.st, nullptr, a.base, a.c, a.layer * 2 * a.c.B, a.prefix_len, 1, ek, (int64_t)(pp * d), kKv4Lop);
     });
     CUtensorMap q, k, v, kt, vt;
     if (!make_map4(&q, a.q, d, n_q, a.B, 1, d, n_q * d, a.B * n_q * d) ||

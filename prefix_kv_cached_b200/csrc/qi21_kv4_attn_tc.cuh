@@ -67,39 +67,6 @@ struct Kv4TcArgs {
     float *part_o;               // [2 grid][slot_rows][DH]
 };
 
-// (nibble - 8) s of the 8 nibbles of a code word as bf16 pairs in the order of dims.
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t s) {
-    uint32_t p;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(p) : "r"(s));
-    return p;
-}
-__device__ __forceinline__ uint32_t kv4_offset_pair(uint32_t s2) {   // -24 s, exact
-    return fma_bf16x2(s2, 0xC1C0C1C0u, 0x80008000u);
-}
-// Nibbles i and i + 4 of w, i = 0 .. 3, as the values of a pair.
-__device__ __forceinline__ uint32_t kv4_nibbles(uint32_t w, const Kv4Lop &k) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(k.mask), "r"(k.one));   // (w & mask) | one
-    return d;
-}
-__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k, uint32_t (&p)[4]) {
-    p[0] = fma_bf16x2(kv4_nibbles(w << 3, k), s2, off2);
-    p[1] = fma_bf16x2(kv4_nibbles(w >> 1, k), s2, off2);
-    p[2] = fma_bf16x2(kv4_nibbles(w >> 5, k), s2, off2);
-    p[3] = fma_bf16x2(kv4_nibbles(w >> 9, k), s2, off2);
-}
-__device__ __forceinline__ uint4 kv4_expand(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k) {
-    uint32_t p[4];
-    kv4_pairs(w, s2, off2, k, p);
-    return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
-                      __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
