@@ -1055,16 +1055,7 @@ extern "C" qi21_status qi21_kv4_evict(const qi21_config *c, const qi21_kv4_cache
     if (src->prefix_len && src->prefix_len == dst->prefix_len) return QI21_ERR_INVALID_ARG;
     dst->state = QI21_CACHE_EMPTY;
     Launcher L((cudaStream_t)stream);
-    const Kv4Dims cd = kv4_dims(*src), od = kv4_dims(*dst);
-    L.run("kv4_select", [&] {
-        k_kv4_select<<<dim3(cd.H, cd.B, c->n_layers), KV4_SEL_THREADS, 0, L.st>>>(scores, cd, src->prefix_len, keep,
-                                                                                n_protected, kept, dst->prefix_len);
-    });
-    L.run("kv4_gather", [&] {
-        const int64_t pieces = (int64_t)keep * (cd.Dh / KV4_GROUP);
-        k_kv4_gather<<<dim3((unsigned)((pieces + 255) / 256), cd.H, c->n_layers * cd.B), 256, 0, L.st>>>(
-            (const uint8_t *)src->base, cd, kept, keep, (uint8_t *)dst->base, od);
-    });
+    launch_kv4_evict(L, *c, *src, scores, keep, n_protected, *dst, kept);
     s = finish(L);
     if (s == QI21_OK) dst->state = QI21_CACHE_EXTRACTED;
     return s;

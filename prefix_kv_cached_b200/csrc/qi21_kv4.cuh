@@ -18,6 +18,7 @@
 // gather. Rows [P, Pp) are never written, and no kernel lets what they (or the
 // rows behind an item's own length) hold reach a result.
 #pragma once
+#include "qi21_attn_tc.cuh"     // packed fp32 pairs
 #include "qi21_common.cuh"
 
 namespace qi21 {
@@ -138,14 +139,22 @@ __device__ __forceinline__ uint32_t kv4_code_word(const float (&x)[8], float s) 
     const float up = r * (1.f + 0x1p-20f), dn = r * (1.f - 0x1p-20f), M = 12582920.f;
     uint32_t b[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float a = fmaf(x[k], up, M), c = fmaf(x[k], dn, M);
-        b[k] = __float_as_uint(a + c);
-        if (EXACT && a != c) {
-            float q = fminf(a, c) - M;                 // the lower of the two integers
-            const float e = fmaf(-q, s, x[k]), h = 0.5f * s;
-            if (e > h || (e == h && ((int)q & 1))) q += 1.f;
-            b[k] = __float_as_uint(2.f * (q + M));
+    for (int k = 0; k < 8; k += 2) {               // packed pairs
+        const uint64_t v = f2_pack(x[k], x[k + 1]);
+        const uint64_t a2 = f2_fma(v, f2_pack(up, up), f2_pack(M, M)), c2 = f2_fma(v, f2_pack(dn, dn), f2_pack(M, M));
+        float a[2], c[2], t[2];
+        f2_unpack(f2_add(a2, c2), t[0], t[1]);
+        f2_unpack(a2, a[0], a[1]);
+        f2_unpack(c2, c[0], c[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            b[k + i] = __float_as_uint(t[i]);
+            if (EXACT && a[i] != c[i]) {
+                float q = fminf(a[i], c[i]) - M;           // the lower of the two integers
+                const float e = fmaf(-q, s, x[k + i]), h = 0.5f * s;
+                if (e > h || (e == h && ((int)q & 1))) q += 1.f;
+                b[k + i] = __float_as_uint(2.f * (q + M));
+            }
         }
     }
     // the low bytes hold the codes: even ones, and odd ones a nibble further
@@ -156,6 +165,7 @@ __device__ __forceinline__ uint32_t kv4_code_word(const float (&x)[8], float s) 
 
 // Bits of the largest magnitude of 8 consecutive elements (a NaN's lie above all others).
 __device__ __forceinline__ uint32_t kv4_max8(const float (&x)[8]) {
+    // (integer maxima of the cleared sign bits)
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
@@ -171,8 +181,8 @@ constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row 
 // threads of a group share its maximum by two shuffles. Bound by HBM: eb + 0.5625
 // bytes an element.
 template <typename T>
-__global__ void __launch_bounds__(256) k_kv4_quantize(const T *__restrict__ src, int64_t slab_stride, Kv4Dims c,
-                                                      const int *__restrict__ prefix_len, uint8_t *__restrict__ base) {
+__global__ void __launch_bounds__(256) k_kv4_quantize(const T *src, int64_t slab_stride, Kv4Dims c,
+                                                      const int *prefix_len, uint8_t *base) {
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t d = c.H * c.Dh, cols = d / 8, u = blockIdx.x * 256 + threadIdx.x;
@@ -244,9 +254,9 @@ __device__ __forceinline__ float kv4_load_scale(const uint8_t *base, const Kv4Di
 // the mapping of k_kv4_quantize. pad: zeros behind them up to a multiple of 128 rows
 // (the tiles of an attention that reads the result).
 template <typename T>
-__global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *__restrict__ base, Kv4Dims c, int slab0,
-                                                        const int *__restrict__ prefix_len, int pad,
-                                                        T *__restrict__ dst, int64_t slab_stride, Kv4Lop lop) {
+__global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *base, Kv4Dims c, int slab0,
+                                                        const int *prefix_len, int pad,
+                                                        T *dst, int64_t slab_stride, Kv4Lop lop) {
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t d = c.H * c.Dh, cols = d / 8, u = blockIdx.x * 256 + threadIdx.x;
@@ -284,105 +294,179 @@ __device__ __forceinline__ uint32_t kv4_rank(float s, int j, int n_protected) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-constexpr int KV4_SEL_THREADS = 512;
-
-// Exclusive prefix sum of a flag over the block (all threads call); *total on every thread.
-__device__ __forceinline__ int kv4_block_rank(bool f, int *warp_sums, int *total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const uint32_t m = __ballot_sync(0xffffffffu, f);
-    __syncthreads();
-    if (lane == 0) warp_sums[wid] = __popc(m);
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < KV4_SEL_THREADS / 32; ++i) {
-        const int n = warp_sums[i];
-        if (i < wid) before += n;
-        all += n;
-    }
-    *total = all;
-    return before + __popc(m & ((1u << lane) - 1));
-}
 
 // The rows that one (layer, item, head) keeps: the `keep` largest of its ranks,
 // ties to the lowest row, in ascending order; -1 behind them where the item has
 // fewer rows. Radix selection, 8 bits a pass from the top, on integers: exact, and
-// the same whatever the order of the atomics. grid (H, B, L).
-__global__ void __launch_bounds__(KV4_SEL_THREADS)
-    k_kv4_select(const float *__restrict__ scores, Kv4Dims c, const int *__restrict__ prefix_len, int keep,
-                 int n_protected, int *__restrict__ kept, int *__restrict__ dst_len) {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[KV4_SEL_THREADS / 32];
-    __shared__ int sel[2];
+// the same whatever the order of the atomics. A thread holds IPT consecutive rows,
+// so that one scan over the block gives every row its place; where the rows are more
+// than THREADS x IPT, they are read again tile by tile in each pass. Bound by latency
+// (barriers and one read of the scores). grid (H, B, L).
+template <int THREADS, int IPT>
+__global__ void __launch_bounds__(THREADS)
+    k_kv4_select(const float *scores, Kv4Dims c, const int *prefix_len, int keep,
+                 int n_protected, int *kept, int *dst_len) {
+    constexpr int W = THREADS / 32, TILE = THREADS * IPT;
+    static_assert(TILE <= 8192, "two counts share 32 bits");
+    __shared__ int hist[2][256];
+    __shared__ int sel[2], warp_sums[W];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    for (int i = tid; i < 512; i += THREADS) hist[i >> 8][i & 255] = 0;
+    pdl_launch_dependents();
+    pdl_wait();
     const int h = blockIdx.x, b = blockIdx.y, l = blockIdx.z;
     const int64_t lbh = ((int64_t)l * c.B + b) * c.H + h;
     const float *sc = scores + lbh * c.P;
     int *out = kept + lbh * keep;
-    const int len = kv4_len(c, prefix_len, b);
-    const int count = min(keep, len);
-    if (dst_len && l == 0 && h == 0 && threadIdx.x == 0) dst_len[b] = count;
+    const int len = kv4_len(c, prefix_len, b), count = min(keep, len), tiles = (len + TILE - 1) / TILE;
+    if (dst_len && l == 0 && h == 0 && tid == 0) dst_len[b] = count;
+    uint32_t key[IPT];
+    auto load = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < IPT; ++i) {
+            const int j = tile * TILE + tid * IPT + i;
+            key[i] = j < len ? kv4_rank(sc[j], j, n_protected) : 0u;
+        }
+    };
+    load(0);
     uint32_t prefix = 0;         // the bits of the count-th largest rank found so far
     int need = count;            // how many ranks with these bits are taken
     if (count < len) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < 256; i += KV4_SEL_THREADS) hist[i] = 0;
-            __syncthreads();
-            const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-            for (int j = threadIdx.x; j < len; j += KV4_SEL_THREADS) {
-                const uint32_t r = kv4_rank(sc[j], j, n_protected);
-                if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & 255], 1);
+#pragma unroll 1
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+            int *hs = hist[pass & 1];
+            __syncthreads();                                   // hs is zero
+            for (int t = 0; t < tiles; ++t) {
+                if (tiles > 1) load(t);
+#pragma unroll
+                for (int i = 0; i < IPT; ++i)
+                    if (t * TILE + tid * IPT + i < len && (key[i] & mask) == prefix)
+                        atomicAdd(&hs[(key[i] >> shift) & 255], 1);
             }
             __syncthreads();
-            if (threadIdx.x == 0) {
-                int n = need, d = 255;
-                while (d > 0 && hist[d] < n) n -= hist[d--];
-                sel[0] = d;
-                sel[1] = n;
+            if (wid == 0) {
+                // 8 bins a lane, the largest ones first: the bin in which the count is reached
+                int n[8], sum = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    n[i] = hs[255 - (lane * 8 + i)];
+                    sum += n[i];
+                }
+                int upto = sum;
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, x);
+                    if (lane >= x) upto += v;
+                }
+                int before = upto - sum;
+                if (before < need && upto >= need) {           // one lane
+                    int i = 0;
+#pragma unroll
+                    for (int k = 0; k < 7; ++k)
+                        if (i == k && before + n[k] < need) {
+                            before += n[k];
+                            ++i;
+                        }
+                    sel[0] = 255 - (lane * 8 + i);
+                    sel[1] = need - before;
+                }
+            } else {
+                for (int i = tid - 32; i < 256; i += THREADS - 32) hist[(pass + 1) & 1][i] = 0;   // for the next pass
             }
             __syncthreads();
             prefix |= (uint32_t)sel[0] << shift;
             need = sel[1];
         }
     }
-    int ties = 0, taken = 0;
-    for (int j0 = 0; j0 < len; j0 += KV4_SEL_THREADS) {
-        const int j = j0 + threadIdx.x;
-        const uint32_t r = j < len ? kv4_rank(sc[j], j, n_protected) : 0u;
-        int n;
-        bool take = j < len;
-        if (count < len) {
-            const bool tie = j < len && r == prefix;
-            const int before = ties + kv4_block_rank(tie, warp_sums, &n);
-            ties += n;
-            take = j < len && (r > prefix || (tie && before < need));
+    // places: the larger ranks before a row, and as many of its ties as are taken
+    int above0 = 0, ties0 = 0;
+    for (int t = 0; t < tiles; ++t) {
+        if (tiles > 1) load(t);
+        const int j0 = t * TILE + tid * IPT;
+        int above = 0, ties = 0;
+#pragma unroll
+        for (int i = 0; i < IPT; ++i) {
+            if (j0 + i >= len) continue;
+            if (count == len || key[i] > prefix) ++above;
+            else if (key[i] == prefix) ++ties;
         }
-        const int at = taken + kv4_block_rank(take, warp_sums, &n);
-        taken += n;
-        if (take && at < count) out[at] = j;
+        int mine = above | (ties << 16), upto = mine;          // at most 8192 of each in a tile
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, x);
+            if (lane >= x) upto += v;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sums[wid] = upto;
+        __syncthreads();
+        int base = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int n = warp_sums[i];
+            if (i < wid) base += n;
+            all += n;
+        }
+        base += upto - mine;
+        int a = above0 + (base & 0xFFFF), q = ties0 + (base >> 16);
+#pragma unroll
+        for (int i = 0; i < IPT; ++i) {
+            if (j0 + i >= len) continue;
+            const bool tie = count < len && key[i] == prefix;
+            const bool take = count == len || key[i] > prefix || (tie && q < need);
+            if (take) out[a + min(q, need)] = j0 + i;
+            if (tie) ++q;
+            else if (take) ++a;
+        }
+        above0 += all & 0xFFFF;
+        ties0 += all >> 16;
     }
-    for (int i = count + threadIdx.x; i < keep; i += KV4_SEL_THREADS) out[i] = -1;
+    for (int i = count + tid; i < keep; i += THREADS) out[i] = -1;
 }
 
+constexpr int KV4_GATHER = 4;    // rows of a thread
+
 // Copy the kept rows of K and V into the smaller cache. A thread moves one group
-// (16 bytes of codes and its scale) of a row of K and of V. grid (pieces, H, L * B).
+// (16 bytes of codes and its scale) of four rows of K and of V, all of them in flight
+// at once. grid (pieces, H, L * B).
 __global__ void __launch_bounds__(256)
-    k_kv4_gather(const uint8_t *__restrict__ src, Kv4Dims c, const int *__restrict__ kept, int keep,
-                 uint8_t *__restrict__ dst, Kv4Dims o) {
-    const int G = c.Dh / KV4_GROUP;
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int r = (int)(u / G), g = (int)(u - (int64_t)r * G);
-    if (r >= keep) return;
+    k_kv4_gather(const uint8_t *src, Kv4Dims c, const int *kept, int keep, uint8_t *dst, Kv4Dims o) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint32_t G = c.Dh / KV4_GROUP, rows = 256 / G;       // G threads a row, `rows` rows at a time
+    const int g = threadIdx.x % G, r0 = blockIdx.x * (KV4_GATHER * rows) + threadIdx.x / G;
+    if (threadIdx.x / G >= rows) return;                       // 256 is no multiple of 3
     const int h = blockIdx.y, l = blockIdx.z / c.B, b = blockIdx.z - l * c.B;
-    const int j = kept[(((int64_t)l * c.B + b) * c.H + h) * keep + r];
-    if (j < 0) return;
+    const int *list = kept + (((int64_t)l * c.B + b) * c.H + h) * keep;
+    int j[KV4_GATHER];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const int64_t from = (kv4_row0(c, l, which, b, h) + j) * G + g, to = (kv4_row0(o, l, which, b, h) + r) * G + g;
-        reinterpret_cast<uint4 *>(dst)[to] = reinterpret_cast<const uint4 *>(src)[from];
-        reinterpret_cast<uint16_t *>(dst + o.scales_off)[to] =
-            reinterpret_cast<const uint16_t *>(src + c.scales_off)[from];
+    for (int i = 0; i < KV4_GATHER; ++i) {
+        const int r = r0 + i * rows;
+        j[i] = r < keep ? list[r] : -1;
     }
+    const uint16_t *from_s = reinterpret_cast<const uint16_t *>(src + c.scales_off);
+    uint16_t *to_s = reinterpret_cast<uint16_t *>(dst + o.scales_off);
+    uint4 code[2][KV4_GATHER];
+    uint16_t scale[2][KV4_GATHER];
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int i = 0; i < KV4_GATHER; ++i)
+            if (j[i] >= 0) {
+                const int64_t from = (kv4_row0(c, l, which, b, h) + j[i]) * G + g;
+                code[which][i] = reinterpret_cast<const uint4 *>(src)[from];
+                scale[which][i] = from_s[from];
+            }
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int i = 0; i < KV4_GATHER; ++i)
+            if (j[i] >= 0) {
+                const int64_t to = (kv4_row0(o, l, which, b, h) + r0 + i * rows) * G + g;
+                reinterpret_cast<uint4 *>(dst)[to] = code[which][i];
+                to_s[to] = scale[which][i];
+            }
 }
 
 // ------------------------------------------------------------------ CUDA-core attention

@@ -323,6 +323,26 @@ static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_
     }
 }
 
+static void launch_kv4_evict(Launcher &L, const qi21_config &c, const qi21_kv4_cache &src, const float *scores,
+                             int keep, int n_protected, const qi21_kv4_cache &dst, int *kept) {
+    const Kv4Dims cd = kv4_dims(src), od = kv4_dims(dst);
+    L.run("kv4_select", [&] {
+        // rows a thread holds: as many as the prefix needs, so that it is read once
+        auto go = [&](auto *kernel, int threads) {
+            launch_dep(kernel, dim3(cd.H, cd.B, c.n_layers), dim3(threads), 0, L.st, nullptr, scores, cd,
+                       src.prefix_len, keep, n_protected, kept, dst.prefix_len);
+        };
+        if (cd.P <= 512) go(k_kv4_select<128, 4>, 128);
+        else if (cd.P <= 2048) go(k_kv4_select<256, 8>, 256);
+        else go(k_kv4_select<512, 16>, 512);
+    });
+    L.run("kv4_gather", [&] {
+        const int rows = KV4_GATHER * (256 / (cd.Dh / KV4_GROUP));           // of a block
+        launch_dep(k_kv4_gather, dim3((keep + rows - 1) / rows, cd.H, c.n_layers * cd.B), dim3(256), 0, L.st, nullptr,
+                   (const uint8_t *)src.base, cd, kept, keep, (uint8_t *)dst.base, od);
+    });
+}
+
 // Shared checks of the attention, the scores and the cached step.
 static qi21_status check_kv4_queries(const qi21_config *c, const qi21_kv4_cache *k, int32_t B, int32_t n_q,
                                      int32_t n_tail) {
