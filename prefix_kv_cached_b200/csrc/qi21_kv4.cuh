@@ -163,14 +163,48 @@ __device__ __forceinline__ uint32_t kv4_code_word(const float (&x)[8], float s) 
     return e + 16u * o;
 }
 
-// Bits of the largest magnitude of 8 consecutive elements (a NaN's lie above all others).
-__device__ __forceinline__ uint32_t kv4_max8(const float (&x)[8]) {
-    // (integer maxima of the cleared sign bits)
-    uint32_t m = 0;
+// 8 consecutive elements as they are stored: the bits (of a float) of the largest
+// magnitude, where a NaN's lie above all others, and the elements as floats.
+template <typename T> struct Kv4Row8;
+template <> struct Kv4Row8<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float *p) { load8(p, x); }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-    return m;
-}
+        for (int k = 0; k < 8; ++k) x[k] = 0.f;
+    }
+    __device__ __forceinline__ uint32_t max_bits() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+        return m;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = x[k];
+    }
+};
+template <> struct Kv4Row8<bf16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const bf16 *p) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+    __device__ __forceinline__ uint32_t max_bits() const {       // both halves of a word at once
+        uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int k = 1; k < 4; ++k) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7FFF7FFFu));
+        return max(m & 0xFFFF0000u, m << 16);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+    }
+};
 
 constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row kernels handles
 
@@ -192,33 +226,33 @@ __global__ void __launch_bounds__(256) k_kv4_quantize(const T *src, int64_t slab
     const uint32_t h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
     const int64_t r0 = (int64_t)quad * KV4_Q_ROWS;
     const T *from = src + slab * slab_stride + r0 * d + col * 8;
-    float x[KV4_Q_ROWS][8];
+    Kv4Row8<T> x[KV4_Q_ROWS];
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        if (r0 + i < rows) {
-            load8(from + (int64_t)i * d, x[i]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
-        }
+        if (r0 + i < rows) x[i].load(from + i * d);
+        else x[i].zero();
     }
     const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp + r0;
-    uint8_t *codes = base + row0 * (c.Dh / 2) + j0 / 2;
-    uint16_t *scales = reinterpret_cast<uint16_t *>(base + c.scales_off) + row0 * (c.Dh / KV4_GROUP) + j0 / KV4_GROUP;
+    const uint32_t row_codes = c.Dh / 2, row_scales = c.Dh / KV4_GROUP;
+    uint8_t *codes = base + row0 * row_codes + j0 / 2;
+    uint16_t *scales = reinterpret_cast<uint16_t *>(base + c.scales_off) + row0 * row_scales + j0 / KV4_GROUP;
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        uint32_t m = kv4_max8(x[i]);
+        uint32_t m = x[i].max_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const float s = kv4_scale(m);
-        if (m > 0x7DE00000u) {                               // beyond 7 * 2^122: saturate
+        float v[8];
+        x[i].get(v);
+        if (__any_sync(0xffffffffu, m > 0x7DE00000u)) {      // beyond 7 * 2^122: saturate
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[i][k] = fminf(fmaxf(x[i][k], -7.f * s), 7.f * s);
+            for (int k = 0; k < 8; ++k) v[k] = fminf(fmaxf(v[k], -7.f * s), 7.f * s);
         }
-        const uint32_t w = s > 0.f ? kv4_code_word<sizeof(T) == 4>(x[i], s) : 0x88888888u;
+        uint32_t w = kv4_code_word<sizeof(T) == 4>(v, s);
+        if (!(s > 0.f)) w = 0x88888888u;                     // an empty group, or one that is not finite
         if (r0 + i < rows) {
-            *reinterpret_cast<uint32_t *>(codes + (int64_t)i * (c.Dh / 2)) = w;
-            if ((col & 3) == 0) scales[(int64_t)i * (c.Dh / KV4_GROUP)] = (uint16_t)(__float_as_uint(s) >> 16);
+            *reinterpret_cast<uint32_t *>(codes + i * row_codes) = w;
+            if ((col & 3) == 0) scales[i * row_scales] = (uint16_t)(__float_as_uint(s) >> 16);
         }
     }
 }
