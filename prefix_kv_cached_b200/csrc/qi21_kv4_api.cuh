@@ -112,7 +112,8 @@ static void launch_kv4_attn_tc(Launcher &L, const Kv4AttnArgs &a, const Kv4Plan 
     }
     if (!p.w.whole && p.w.grid > 1)
         L.run("kv4_join", [&] {
-            launch_dep(k_kv4_join<DH>, dim3((p.w.slot_rows + 7) / 8, p.w.grid - 1), dim3(256), 0, L.st, nullptr, p);
+            launch_dep(k_kv4_join<DH>, dim3((p.w.slot_rows + 8 * KV4_JOIN_ROWS - 1) / (8 * KV4_JOIN_ROWS), p.w.grid - 1),
+                       dim3(256), 0, L.st, nullptr, p);
         });
 }
 

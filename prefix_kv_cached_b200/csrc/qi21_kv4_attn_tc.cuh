@@ -57,7 +57,9 @@ struct Kv4AttnCfg {
 
 // First step of a CTA's range (kv4_plan() fills Kv4Work).
 __host__ __device__ __forceinline__ int64_t kv4_work_begin(const Kv4Work &w, int cta) {
-    return w.whole ? (int64_t)cta * w.units / w.grid * w.tiles : (int64_t)cta * ((int64_t)w.units * w.tiles) / w.grid;
+    const int64_t n = w.whole ? w.units : (int64_t)w.units * w.tiles, p = n * cta;
+    const int64_t at = (p >> 32) == 0 ? (int64_t)((uint32_t)p / (uint32_t)w.grid) : p / w.grid;   // 32 bits are cheaper
+    return w.whole ? at * w.tiles : at;
 }
 
 struct Kv4TcArgs {
@@ -135,10 +137,14 @@ __device__ __forceinline__ Kv4Seg kv4_segment(const Kv4TcArgs &p, int64_t at, in
     return s;
 }
 
+// Steps of a segment that hold prefix rows; they come first.
+__device__ __forceinline__ int kv4_prefix_steps(const Kv4TcArgs &p, const Kv4Seg &s) {
+    return max(0, min(s.t1, min(p.w.tiles_p, (s.len + 127) >> 7)) - s.t0);
+}
+
 // Step number n (0 .. n_valid) of a segment: prefix tile (< tiles_p) or tail tile.
 __device__ __forceinline__ int kv4_step_tile(const Kv4TcArgs &p, const Kv4Seg &s, int n) {
-    const int tp = min(p.w.tiles_p, (s.len + 127) >> 7);
-    const int in_prefix = max(0, min(s.t1, tp) - s.t0);
+    const int in_prefix = kv4_prefix_steps(p, s);
     return n < in_prefix ? s.t0 + n : max(s.t0, p.w.tiles_p) + (n - in_prefix);
 }
 
@@ -407,6 +413,9 @@ __global__ void __launch_bounds__(512, 1)
             const int nA = KH ? (seg.n_valid + 1) >> 1 : seg.n_valid;
             const int nB = KH ? seg.n_valid >> 1 : (seg.rows > 128 ? seg.n_valid : 0);
             const int nt = h ? nB : nA, n0 = KH && h ? nA : 0;
+            // keys of step n: (n < n_pre ? keys_p : keys_t) - 128 n
+            const int n_pre = kv4_prefix_steps(p, seg), keys_p = seg.len - (seg.t0 + n0) * C::BK;
+            const int keys_t = p.a.n_tail - (max(seg.t0, p.w.tiles_p) - p.w.tiles_p - n_pre + n0) * C::BK;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < nt && ok; ++j, ++ns) {
                 if (!(ok = wait_all(&s_full[h], ns & 1))) break;
@@ -415,8 +424,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) tmem_ld32(t_s + cc * 32, sv[cc]);
                 tmem_wait_ld();
-                const int tile = kv4_step_tile(p, seg, n0 + j);
-                const int n_keys = tile < p.w.tiles_p ? seg.len - tile * 128 : p.a.n_tail - (tile - p.w.tiles_p) * 128;
+                const int n_keys = (n0 + j < n_pre ? keys_p : keys_t) - j * C::BK;
                 if (n_keys < C::BK) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
@@ -424,12 +432,11 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 float m4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m4[i] = -INFINITY;
+                for (int i = 0; i < 4; ++i) m4[i] = fmaxf(sv[0][2 * i], sv[0][2 * i + 1]);
 #pragma unroll
-                for (int i = 0; i < 128; i += 2)
-                    m4[(i >> 1) & 3] = fmax3_nan(m4[(i >> 1) & 3], sv[i >> 5][i & 31], sv[i >> 5][(i + 1) & 31]);
-                const float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
-                if (mx != mx) l_run = mx;      // the polynomial exponential would lose a NaN score
+                for (int i = 8; i < 128; i += 2)
+                    m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], sv[i >> 5][i & 31], sv[i >> 5][(i + 1) & 31]);
+                const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
                 // move the running max only when this tile raises it by more than 2^8
                 const bool first = (m_run == -INFINITY);
                 const bool grow = first || (mx - m_run) * c > kRescaleLog2;
@@ -454,12 +461,11 @@ __global__ void __launch_bounds__(512, 1)
                     for (int q = 0; q < 16; ++q) {
                         float x0, x1, e0, e1;
                         f2_unpack(f2_fma(f2_pack(sv[cc][2 * q], sv[cc][2 * q + 1]), c2, nmc2), x0, x1);
-                        if ((cc * 16 + q) % kPolyEvery == kPolyEvery - 1) {
-                            ex2_poly2_deg<4>(x0, x1, e0, e1);
-                        } else {
-                            e0 = ex2_approx(x0);
-                            e1 = ex2_approx(x1);
-                        }
+                        // all on the MUFU units: with every 8th pair on the FMA pipe the
+                        // expansion has less of the issue slots (175 us against 157; 256 rows,
+                        // 32 heads of 128, P 33792). A NaN score makes its row's sum one.
+                        e0 = ex2_approx(x0);
+                        e1 = ex2_approx(x1);
                         s4[q & 3] = f2_add(s4[q & 3], f2_pack(e0, e1));
                         u[q] = pack_bf16x2(e0, e1);
                     }
@@ -572,45 +578,79 @@ __global__ void __launch_bounds__(512, 1)
 
 // Join the partial results of the units that the sharing cut. Block y stands for
 // the boundary in front of CTA y + 1: where it is the first one inside a unit, its
-// warps (one per query row) go through the CTAs that share the unit, in order.
+// warps go through the CTAs that share the unit, in order, four query rows at a time.
+constexpr int KV4_JOIN_ROWS = 4;
+
 template <int DH>
-__global__ void __launch_bounds__(256) k_kv4_join(Kv4TcArgs p) {
+__global__ void __launch_bounds__(256) k_kv4_join(const __grid_constant__ Kv4TcArgs p) {
     pdl_launch_dependents();
     pdl_wait();
+    constexpr int R = KV4_JOIN_ROWS, C = DH / 32;
     const int c1 = blockIdx.y + 1, T = p.w.tiles;
     const int64_t edge = kv4_work_begin(p.w, c1);
     const int unit = (int)(edge / T);
-    if (edge == (int64_t)unit * T) return;
-    if (kv4_work_begin(p.w, c1 - 1) > (int64_t)unit * T) return;   // an earlier boundary of the unit
-    const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t begin = (int64_t)unit * T, end = begin + T;
+    if (edge == begin || kv4_work_begin(p.w, c1 - 1) > begin) return;   // not inside, or not the first
+    const int lane = threadIdx.x & 31, r0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * R;
     const int qt = unit % p.w.q_tiles, bh = unit / p.w.q_tiles, h = bh % p.a.c.H, b = bh / p.a.c.H;
-    const int row = qt * p.w.unit_rows + r;
-    if (r >= p.w.unit_rows || row >= p.a.n_q) return;
-    const int64_t end = (int64_t)(unit + 1) * T;
-    // CTA c's partial of this unit: its first segment (slot 0) unless the unit begins inside its range
-    auto slot = [&](int c) -> int64_t {
-        const int64_t lo = kv4_work_begin(p.w, c);
-        return ((int64_t)2 * c + (lo < (int64_t)unit * T ? 1 : 0)) * p.w.slot_rows + r;
-    };
-    float m = -INFINITY;
-    for (int c = c1 - 1; c < p.w.grid && kv4_work_begin(p.w, c) < end; ++c) m = fmaxf(m, p.part_l[slot(c)]);
-    const float mz = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, o[DH / 32];
+    const int row0 = qt * p.w.unit_rows + r0, live = min(min(R, p.w.unit_rows - r0), p.a.n_q - row0);
+    if (live <= 0) return;
+    float m[R], sum[R], o[R][C];
 #pragma unroll
-    for (int j = 0; j < DH / 32; ++j) o[j] = 0.f;
-    for (int c = c1 - 1; c < p.w.grid && kv4_work_begin(p.w, c) < end; ++c) {
-        const int64_t at = slot(c);
-        const float w = exp2f(p.part_l[at] - mz);
-        sum += w;
+    for (int k = 0; k < R; ++k) {
+        m[k] = -INFINITY;
+        sum[k] = 0.f;
 #pragma unroll
-        for (int j = 0; j < DH / 32; ++j) o[j] = fmaf(w, p.part_o[at * DH + lane + 32 * j], o[j]);
+        for (int j = 0; j < C; ++j) o[k][j] = 0.f;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    bf16 *dst = (bf16 *)p.a.out + ((int64_t)b * p.a.n_q + row) * ((int64_t)p.a.c.H * DH) + h * DH;
+    // The CTAs that share the unit, one a lane (32 at a time): CTA c's partial result is
+    // in its slot 0 (its first segment) unless the unit begins inside its range.
+    for (int c0 = c1 - 1; c0 < p.w.grid && kv4_work_begin(p.w, c0) < end; c0 += 32) {
+        const int c = c0 + lane;
+        const int64_t lo = kv4_work_begin(p.w, c);
+        const bool in = c < p.w.grid && lo < end;
+        const int slot = 2 * c + (lo < begin ? 1 : 0);
+        const int n = __popc(__ballot_sync(0xffffffffu, in));
+        float w[R];
 #pragma unroll
-    for (int j = 0; j < DH / 32; ++j) dst[lane + 32 * j] = __float2bfloat16_rn(o[j] * inv);
-    if (p.a.lse && lane == 0)
-        p.a.lse[((int64_t)h * p.a.B + b) * p.a.n_q + row] = sum == 0.f ? -INFINITY : (mz + log2f(sum)) * KV4_LN2;
+        for (int k = 0; k < R; ++k)
+            w[k] = in && k < live ? p.part_l[(int64_t)slot * p.w.slot_rows + r0 + k] : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const float mn = fmaxf(m[k], warp_max(w[k])), mz = mn == -INFINITY ? 0.f : mn;
+            const float scale = exp2f(m[k] - mz);              // of what earlier ones gave
+            w[k] = in ? exp2f(w[k] - mz) : 0.f;
+            m[k] = mn;
+            sum[k] = sum[k] * scale + warp_sum(w[k]);
+#pragma unroll
+            for (int j = 0; j < C; ++j) o[k][j] *= scale;
+        }
+        for (int i = 0; i < n; ++i) {
+            const float *src = p.part_o + ((int64_t)__shfl_sync(0xffffffffu, slot, i) * p.w.slot_rows + r0) * DH + lane;
+            float v[R][C];
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int j = 0; j < C; ++j) v[k][j] = k < live ? src[k * DH + 32 * j] : 0.f;
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const float wi = __shfl_sync(0xffffffffu, w[k], i);
+#pragma unroll
+                for (int j = 0; j < C; ++j) o[k][j] = fmaf(wi, v[k][j], o[k][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        if (k >= live) continue;
+        const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+        bf16 *dst = (bf16 *)p.a.out + ((int64_t)b * p.a.n_q + row0 + k) * ((int64_t)p.a.c.H * DH) + h * DH;
+#pragma unroll
+        for (int j = 0; j < C; ++j) dst[lane + 32 * j] = __float2bfloat16_rn(o[k][j] * inv);
+        if (p.a.lse && lane == 0)
+            p.a.lse[((int64_t)h * p.a.B + b) * p.a.n_q + row0 + k] =
+                sum[k] == 0.f ? -INFINITY : (m[k] + log2f(sum[k])) * KV4_LN2;
+    }
 }
 
 }  // namespace qi21
