@@ -148,6 +148,20 @@ __device__ __forceinline__ int kv4_step_tile(const Kv4TcArgs &p, const Kv4Seg &s
     return n < in_prefix ? s.t0 + n : max(s.t0, p.w.tiles_p) + (n - in_prefix);
 }
 
+// Order of the 2 n loads of a segment: K0 K1 V0 K2 V1 .. V(n-1). A K tile is wanted
+// one product earlier than the V tile of the step before it, which is only free when
+// that step's weights are done. Returns 0 for K, 1 for V; j: the step in load order.
+__device__ __forceinline__ int kv4_load_order(int i, int n, int &j) {
+    const int v = i == 2 * n - 1 ? 1 : (i == 0 ? 0 : (i & 1) ^ 1);
+    j = i == 2 * n - 1 ? n - 1 : (i == 0 ? 0 : (i & 1 ? (i + 1) >> 1 : (i >> 1) - 1));
+    return v;
+}
+// Step that is loaded at position j: in the KH arrangement A0 B0 A1 B1 .. of the halves.
+template <bool KH>
+__device__ __forceinline__ int kv4_step_number(int j, int n) {
+    return KH ? ((j & 1) ? ((n + 1) >> 1) + (j >> 1) : (j >> 1)) : j;
+}
+
 template <int DH, bool KH>    // KH: the halves share the rows and split the keys
 __global__ void __launch_bounds__(512, 1)
     k_kv4_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -308,25 +322,22 @@ __global__ void __launch_bounds__(512, 1)
             for (int64_t at = w_lo; at < w_hi && ok;) {
                 const Kv4Seg seg = kv4_segment(p, at, w_hi);
                 at = seg.next;
-                const int nA = (seg.n_valid + 1) >> 1;
-                for (int j = 0; j < seg.n_valid && ok; ++j) {
-                    const int tile = kv4_step_tile(p, seg, KH ? ((j & 1) ? nA + (j >> 1) : (j >> 1)) : j);
+                for (int i = 0; i < 2 * seg.n_valid && ok; ++i) {
+                    int j;
+                    const int which = kv4_load_order(i, seg.n_valid, j);
+                    const int tile = kv4_step_tile(p, seg, kv4_step_number<KH>(j, seg.n_valid));
                     if (tile >= p.w.tiles_p) continue;
-                    for (int which = 0; which < 2; ++which, ++n) {
-                        const uint32_t s = n % C::NS;
-                        if (!mbar_wait(smem_u32(&st_empty[s]), ((n / C::NS) & 1) ^ 1, abort_flag, p.a.err)) {
-                            ok = false;
-                            break;
-                        }
-                        const int64_t row = kv4_row0(p.a.c, p.a.layer, which, p.a.shared ? 0 : seg.b, seg.h) +
-                                            (int64_t)tile * 128;
-                        const uint32_t bar = smem_u32(&st_full[s]);
-                        const uint32_t dst = smem_u32(smem + C::OFF_ST + s * C::STAGE_BYTES);
-                        mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
-                        bulk_load(dst, p.a.base + row * (DH / 2), C::CODE_BYTES, bar);
-                        bulk_load(dst + C::CODE_BYTES, p.a.base + p.a.c.scales_off + row * (C::G * 2), C::SCALE_BYTES,
-                                  bar);
-                    }
+                    const uint32_t s = n % C::NS;
+                    ok = mbar_wait(smem_u32(&st_empty[s]), ((n / C::NS) & 1) ^ 1, abort_flag, p.a.err);
+                    if (!ok) break;
+                    const int64_t row = kv4_row0(p.a.c, p.a.layer, which, p.a.shared ? 0 : seg.b, seg.h) +
+                                        (int64_t)tile * 128;
+                    const uint32_t bar = smem_u32(&st_full[s]);
+                    const uint32_t dst = smem_u32(smem + C::OFF_ST + s * C::STAGE_BYTES);
+                    mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+                    bulk_load(dst, p.a.base + row * (DH / 2), C::CODE_BYTES, bar);
+                    bulk_load(dst + C::CODE_BYTES, p.a.base + p.a.c.scales_off + row * (C::G * 2), C::SCALE_BYTES, bar);
+                    ++n;
                 }
             }
         } else if (warp == 14 && lane == 0) {
@@ -356,43 +367,41 @@ __global__ void __launch_bounds__(512, 1)
         for (int64_t at = w_lo; at < w_hi && ok;) {
             const Kv4Seg seg = kv4_segment(p, at, w_hi);
             at = seg.next;
-            const int nA = (seg.n_valid + 1) >> 1;
-            for (int j = 0; j < seg.n_valid && ok; ++j, ++n) {
-                const int tile = kv4_step_tile(p, seg, KH ? ((j & 1) ? nA + (j >> 1) : (j >> 1)) : j);
-                const uint32_t s = n & 1, par = ((n >> 1) & 1) ^ 1;
 #pragma unroll 1
-                for (int which = 0; which < 2; ++which) {
-                    uint64_t *full = which ? &v_full[s] : &k_full[s], *empty = which ? &v_empty[s] : &k_empty[s];
-                    uint8_t *dst = smem + (which ? C::OFF_V : C::OFF_K) + s * C::KV_BYTES;
-                    if (!(ok = wait_all(empty, par))) break;
-                    if (tile < p.w.tiles_p) {
-                        const uint32_t ss = st % C::NS;
-                        if (!(ok = wait_all(&st_full[ss], (st / C::NS) & 1))) break;
-                        {
-                            const uint8_t *stage = smem + C::OFF_ST + ss * C::STAGE_BYTES;
-                            kv4_expand_tile<DH, 4>(dst, stage, stage + C::CODE_BYTES, seg.len - tile * 128, warp - 8,
-                                                   lane, p.a.lop);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(smem_u32(&st_empty[ss]));
-                            mbar_arrive(smem_u32(full));
-                        }
-                        ++st;
-                    } else if (lane == 0) {
-                        const uint32_t bar = smem_u32(full);
-                        if (warp == 8) {
-                            mbar_arrive_expect_tx(bar, C::KV_BYTES);
-                            for (int x = 0; x < C::BOXES; ++x)
-                                tma_load_4d(smem_u32(dst + x * (C::BK * 128)), which ? &tmV : &tmK, bar,
-                                            seg.h * DH + x * 64, (tile - p.w.tiles_p) * 128, seg.b, 0);
-                        } else {
-                            mbar_arrive(bar);
-                        }
+            for (int i = 0; i < 2 * seg.n_valid; ++i) {
+                int j;
+                const int which = kv4_load_order(i, seg.n_valid, j);
+                const int tile = kv4_step_tile(p, seg, kv4_step_number<KH>(j, seg.n_valid));
+                const uint32_t s = (n + j) & 1, par = (((n + j) >> 1) & 1) ^ 1;
+                uint64_t *full = which ? &v_full[s] : &k_full[s], *empty = which ? &v_empty[s] : &k_empty[s];
+                uint8_t *dst = smem + (which ? C::OFF_V : C::OFF_K) + s * C::KV_BYTES;
+                if (!(ok = wait_all(empty, par))) break;
+                if (tile < p.w.tiles_p) {
+                    const uint32_t ss = st % C::NS;
+                    if (!(ok = wait_all(&st_full[ss], (st / C::NS) & 1))) break;
+                    const uint8_t *stage = smem + C::OFF_ST + ss * C::STAGE_BYTES;
+                    kv4_expand_tile<DH, 4>(dst, stage, stage + C::CODE_BYTES, seg.len - tile * 128, warp - 8, lane,
+                                           p.a.lop);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&st_empty[ss]));
+                        mbar_arrive(smem_u32(full));
+                    }
+                    ++st;
+                } else if (lane == 0) {
+                    const uint32_t bar = smem_u32(full);
+                    if (warp == 8) {
+                        mbar_arrive_expect_tx(bar, C::KV_BYTES);
+                        for (int x = 0; x < C::BOXES; ++x)
+                            tma_load_4d(smem_u32(dst + x * (C::BK * 128)), which ? &tmV : &tmK, bar, seg.h * DH + x * 64,
+                                        (tile - p.w.tiles_p) * 128, seg.b, 0);
+                    } else {
+                        mbar_arrive(bar);
                     }
                 }
             }
+            n += seg.n_valid;
         }
     } else {
         // ---------------------------------------------------------------- softmax (warps 0..7)
