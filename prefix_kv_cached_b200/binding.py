@@ -168,12 +168,11 @@ def check(fn: str, status: int) -> int:
 
 
 def _addr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
+    p = getattr(x, "data_ptr", None)
+    if p is not None:
+        return p()
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(type(x))
@@ -381,26 +380,26 @@ def qi21_kv4_step_workspace_bytes(cfg, batch, n_prefix, n_target):
 
 
 def qi21_kv4_quantize(cfg, cache, cache4, stream=0):
-    return lib.qi21_kv4_quantize(ct.byref(cfg), ct.byref(cache), ct.byref(cache4), stream)
+    return lib.qi21_kv4_quantize(cfg, cache, cache4, stream)
 
 
 def qi21_kv4_dequantize(cfg, cache4, cache, stream=0):
-    return lib.qi21_kv4_dequantize(ct.byref(cfg), ct.byref(cache4), ct.byref(cache), stream)
+    return lib.qi21_kv4_dequantize(cfg, cache4, cache, stream)
 
 
 def qi21_kv4_attention(cfg, cache4, layer, q, batch, n_q, k_tail, v_tail, n_tail, out, lse, ws, ws_bytes, stream=0):
-    return lib.qi21_kv4_attention(ct.byref(cfg), ct.byref(cache4), layer, _addr(q), batch, n_q, _addr(k_tail),
+    return lib.qi21_kv4_attention(cfg, cache4, layer, _addr(q), batch, n_q, _addr(k_tail),
                                   _addr(v_tail), n_tail, _addr(out), _addr(lse), _addr(ws), ws_bytes, stream)
 
 
 def qi21_kv4_scores(cfg, cache4, layer, q, batch, n_q, lse, scores_in, scores_out, ws, ws_bytes, stream=0):
-    return lib.qi21_kv4_scores(ct.byref(cfg), ct.byref(cache4), layer, _addr(q), batch, n_q, _addr(lse),
+    return lib.qi21_kv4_scores(cfg, cache4, layer, _addr(q), batch, n_q, _addr(lse),
                                _addr(scores_in), _addr(scores_out), _addr(ws), ws_bytes, stream)
 
 
 def qi21_kv4_evict(cfg, cache4, scores, keep, n_protected, cache4_out, kept, stream=0):
-    return lib.qi21_kv4_evict(ct.byref(cfg), ct.byref(cache4), _addr(scores), keep, n_protected,
-                              ct.byref(cache4_out), _addr(kept), stream)
+    return lib.qi21_kv4_evict(cfg, cache4, _addr(scores), keep, n_protected,
+                              cache4_out, _addr(kept), stream)
 
 
 def qi21_cached_step_kv4(cfg, weights, cache4, batch, n_target, x_k, cos_sin_target, mod_row_target, scale_final,

@@ -206,53 +206,60 @@ template <> struct Kv4Row8<bf16> {
     }
 };
 
-constexpr int KV4_Q_ROWS = 4;    // rows of one column that a thread of the row kernels handles
+constexpr int KV4_Q_ROWS = 2;    // rows of one column that a thread of the quantiser handles
+constexpr int KV4_D_ROWS = 4;    // and of the way back
 
 // Quantise rows [0, P) of every (layer, K|V, item) slab of a cache in token-major
-// layout (slab stride in elements) into the 4-bit layout. A thread takes 8
-// consecutive dims of 4 consecutive rows (16 bytes a row in bf16; the four scales
-// of a row quad and column share a 32-byte sector at head_dim 128), the four
-// threads of a group share its maximum by two shuffles. Bound by HBM: eb + 0.5625
-// bytes an element.
+// layout (slab stride in elements) into the 4-bit layout. A thread takes 16
+// consecutive dims of two consecutive rows; the two threads of a group share its
+// maximum by a shuffle. Bound by the issue slots (some 6 operations an element), HBM
+// close behind (eb + 0.5625 bytes an element): 139 us with 8 dims a thread, whose
+// scale costs as much, for 277 M elements of bf16, of which 109 us are HBM's.
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv4_quantize(const T *src, int64_t slab_stride, Kv4Dims c,
                                                       const int *prefix_len, uint8_t *base) {
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t d = c.H * c.Dh, cols = d / 8, u = blockIdx.x * 256 + threadIdx.x;
+    const uint32_t d = c.H * c.Dh, cols = d / 16, u = blockIdx.x * 256 + threadIdx.x;
     const int slab = blockIdx.y;                 // (l * 2 + which) * B + b
     const int rows = kv4_len(c, prefix_len, slab % c.B);
-    const uint32_t quad = u / cols, col = u - quad * cols;   // the 4 threads of a group share a warp: cols % 4 == 0
-    const uint32_t h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
-    const int64_t r0 = (int64_t)quad * KV4_Q_ROWS;
-    const T *from = src + slab * slab_stride + r0 * d + col * 8;
-    Kv4Row8<T> x[KV4_Q_ROWS];
+    const uint32_t pair = u / cols, col = u - pair * cols;   // the 2 threads of a group share a warp: cols % 2 == 0
+    const uint32_t h = col * 16 / c.Dh, j0 = col * 16 - h * c.Dh;
+    const int64_t r0 = (int64_t)pair * KV4_Q_ROWS;
+    const T *from = src + slab * slab_stride + r0 * d + col * 16;
+    Kv4Row8<T> x[KV4_Q_ROWS][2];
 #pragma unroll
-    for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        if (r0 + i < rows) x[i].load(from + i * d);
-        else x[i].zero();
-    }
+    for (int i = 0; i < KV4_Q_ROWS; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (r0 + i < rows) x[i][k].load(from + i * d + k * 8);
+            else x[i][k].zero();
+        }
     const int64_t row0 = ((int64_t)slab * c.H + h) * c.Pp + r0;
     const uint32_t row_codes = c.Dh / 2, row_scales = c.Dh / KV4_GROUP;
     uint8_t *codes = base + row0 * row_codes + j0 / 2;
     uint16_t *scales = reinterpret_cast<uint16_t *>(base + c.scales_off) + row0 * row_scales + j0 / KV4_GROUP;
 #pragma unroll
     for (int i = 0; i < KV4_Q_ROWS; ++i) {
-        uint32_t m = x[i].max_bits();
+        uint32_t m = max(x[i][0].max_bits(), x[i][1].max_bits());
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const float s = kv4_scale(m);
-        float v[8];
-        x[i].get(v);
-        if (__any_sync(0xffffffffu, m > 0x7DE00000u)) {      // beyond 7 * 2^122: saturate
+        const bool huge = __any_sync(0xffffffffu, m > 0x7DE00000u);     // beyond 7 * 2^122: saturate
+        uint32_t w[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = fminf(fmaxf(v[k], -7.f * s), 7.f * s);
+        for (int k = 0; k < 2; ++k) {
+            float v[8];
+            x[i][k].get(v);
+            if (huge) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(v[e], -7.f * s), 7.f * s);
+            }
+            w[k] = kv4_code_word<sizeof(T) == 4>(v, s);
+            if (!(s > 0.f)) w[k] = 0x88888888u;              // an empty group, or one that is not finite
         }
-        uint32_t w = kv4_code_word<sizeof(T) == 4>(v, s);
-        if (!(s > 0.f)) w = 0x88888888u;                     // an empty group, or one that is not finite
         if (r0 + i < rows) {
-            *reinterpret_cast<uint32_t *>(codes + i * row_codes) = w;
-            if ((col & 3) == 0) scales[i * row_scales] = (uint16_t)(__float_as_uint(s) >> 16);
+            *reinterpret_cast<uint2 *>(codes + i * row_codes) = make_uint2(w[0], w[1]);
+            if ((col & 1) == 0) scales[i * row_scales] = (uint16_t)(__float_as_uint(s) >> 16);
         }
     }
 }
@@ -285,7 +292,7 @@ __device__ __forceinline__ float kv4_load_scale(const uint8_t *base, const Kv4Di
 }
 
 // The way back: rows [0, len) of slabs slab0, slab0 + 1, .. in token-major layout,
-// the mapping of k_kv4_quantize. pad: zeros behind them up to a multiple of 128 rows
+// 8 dims of four rows a thread. pad: zeros behind them up to a multiple of 128 rows
 // (the tiles of an attention that reads the result).
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *base, Kv4Dims c, int slab0,
@@ -298,14 +305,14 @@ __global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *base, Kv4
     const int rows = kv4_len(c, prefix_len, slab % c.B);
     const uint32_t quad = u / cols, col = u - quad * cols;
     const uint32_t h = col * 8 / c.Dh, j0 = col * 8 - h * c.Dh;
-    const int64_t r0 = (int64_t)quad * KV4_Q_ROWS, row0 = ((int64_t)slab * c.H + h) * c.Pp + r0;
+    const int64_t r0 = (int64_t)quad * KV4_D_ROWS, row0 = ((int64_t)slab * c.H + h) * c.Pp + r0;
     const uint8_t *codes = base + row0 * (c.Dh / 2) + j0 / 2;
     const uint16_t *scales =
         reinterpret_cast<const uint16_t *>(base + c.scales_off) + row0 * (c.Dh / KV4_GROUP) + j0 / KV4_GROUP;
     const int64_t rows_out = pad ? kv4_pad(rows) : rows;
-    uint32_t w[KV4_Q_ROWS], s[KV4_Q_ROWS];
+    uint32_t w[KV4_D_ROWS], s[KV4_D_ROWS];
 #pragma unroll
-    for (int i = 0; i < KV4_Q_ROWS; ++i) {
+    for (int i = 0; i < KV4_D_ROWS; ++i) {
         w[i] = s[i] = 0;                         // the value 0
         if (r0 + i < rows) {
             w[i] = *reinterpret_cast<const uint32_t *>(codes + (int64_t)i * (c.Dh / 2));
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(256) k_kv4_dequantize(const uint8_t *base, Kv4
     }
     T *to = dst + (int64_t)blockIdx.y * slab_stride + r0 * d + col * 8;
 #pragma unroll
-    for (int i = 0; i < KV4_Q_ROWS; ++i)
+    for (int i = 0; i < KV4_D_ROWS; ++i)
         if (r0 + i < rows_out) kv4_store8(to + (int64_t)i * d, w[i], s[i], lop);
 }
 

@@ -27,7 +27,7 @@ static qi21_status check_kv4(const qi21_config *c, const qi21_kv4_cache *k) {
         k->n_prefix <= 0 || k->n_prefix > INT32_MAX - 128)
         return QI21_ERR_CACHE_STATE;
     if ((int64_t)k->n_layers * 2 * k->batch > 65535 || k->n_heads > 65535) return QI21_ERR_SHAPE;
-    // a slab's units of 8 dims by 4 rows are counted in 32 bits
+    // a slab's units of 32 elements are counted in 32 bits
     if (((int64_t)k->n_prefix + 131) / 4 * (c->d_model / 8) > UINT32_MAX - 256ll) return QI21_ERR_SHAPE;
     return QI21_OK;
 }
@@ -43,8 +43,9 @@ static int64_t kv_slab_rows(const qi21_kv_cache &a) {
                            : (int64_t)a.n_prefix + a.n_target;
 }
 
-static dim3 kv4_row_grid(const qi21_config &c, const qi21_kv4_cache &k) {
-    const int64_t units = ((int64_t)k.n_prefix + KV4_Q_ROWS - 1) / KV4_Q_ROWS * (c.d_model / 8);
+// A thread for every `rows` rows by `dims` dims of a slab.
+static dim3 kv4_row_grid(const qi21_config &c, const qi21_kv4_cache &k, int rows, int dims) {
+    const int64_t units = ((int64_t)k.n_prefix + rows - 1) / rows * (c.d_model / dims);
     return dim3((unsigned)((units + 255) / 256), (unsigned)(c.n_layers * 2 * k.batch));
 }
 
@@ -52,7 +53,7 @@ template <typename T>
 static void launch_kv4_quantize(Launcher &L, const qi21_config &c, const qi21_kv_cache &src,
                                 const qi21_kv4_cache &dst) {
     L.run("kv4_quantize", [&] {
-        launch_dep(k_kv4_quantize<T>, kv4_row_grid(c, dst), dim3(256), 0, L.st, nullptr, (const T *)src.base,
+        launch_dep(k_kv4_quantize<T>, kv4_row_grid(c, dst, KV4_Q_ROWS, 16), dim3(256), 0, L.st, nullptr, (const T *)src.base,
                    kv_slab_rows(src) * c.d_model, kv4_dims(dst), dst.prefix_len, (uint8_t *)dst.base);
     });
 }
@@ -61,7 +62,7 @@ template <typename T>
 static void launch_kv4_dequantize(Launcher &L, const qi21_config &c, const qi21_kv4_cache &src,
                                   const qi21_kv_cache &dst) {
     L.run("kv4_dequantize", [&] {
-        launch_dep(k_kv4_dequantize<T>, kv4_row_grid(c, src), dim3(256), 0, L.st, nullptr, (const uint8_t *)src.base,
+        launch_dep(k_kv4_dequantize<T>, kv4_row_grid(c, src, KV4_D_ROWS, 8), dim3(256), 0, L.st, nullptr, (const uint8_t *)src.base,
                    kv4_dims(src), 0, src.prefix_len, 0, (T *)dst.base, kv_slab_rows(dst) * c.d_model, kKv4Lop);
     });
 }
@@ -151,7 +152,7 @@ template <int DH>
 static void launch_kv4_attn_expanded(Launcher &L, const Kv4AttnArgs &a, const Kv4Plan &plan, char *ws) {
     const uint64_t d = (uint64_t)a.c.H * DH, n_q = a.n_q, nt = a.n_tail > 0 ? a.n_tail : n_q, pp = a.c.Pp;
     bf16 *ek = (bf16 *)(ws + plan.expand), *ev = ek + a.c.B * pp * d;
-    const int64_t quads = pp / KV4_Q_ROWS;
+    const int64_t quads = pp / KV4_D_ROWS;
     L.run("kv4_expand", [&] {
         launch_dep(k_kv4_dequantize<bf16>, dim3((unsigned)((quads * (d / 8) + 255) / 256), 2 * a.c.B), dim3(256), 0,
                    L.st, nullptr, a.base, a.c, a.layer * 2 * a.c.B, a.prefix_len, 1, ek, (int64_t)(pp * d), kKv4Lop);
