@@ -297,6 +297,92 @@ def test_attention_scores_of_very_different_size(B, mode, N):
         assert np.abs(_np(lse)[h, 0] - ls).max() <= LSE_ABS + ds
 
 
+@pytest.mark.parametrize("mode", ["f32", "bf16_cuda_cores"], indirect=True)
+@pytest.mark.parametrize("H,Dh,P,N,T,lens", [(8, 32, 131, 45, 20, None), (8, 96, 70, 33, 0, [70, 9]),
+                                             (8, 32, 3, 1, 1, [0, 3]), (8, 96, 400, 2, 65, None)])
+def test_attention_scores_and_eviction_at_other_head_dims(B, mode, H, Dh, P, N, T, lens):
+    """head_dim 32 and 96, which the CUDA-core family covers."""
+    dtype, tdt = mode
+    cfg = _cfg(B, dtype, H, Dh)
+    rng = np.random.default_rng(Dh + P)
+    buf, vals = _kv4.make_buffer(rng, B, cfg, 2, P, lens)
+    lt = _lens_t(lens)
+    k4 = B.qi21_kv4_cache_init(buf, cfg, 2, P, lt)
+    k4.state = B.QI21_CACHE_EXTRACTED
+    draw = lambda n, s: torch.from_numpy(rng.standard_normal((2, n, H * Dh)) * s).to(tdt).cuda()  # noqa: E731
+    q, kt, vt = draw(N, 1.5), draw(T, 1.0) if T else None, draw(T, 1.0) if T else None
+    out, lse = _run_attention(B, cfg, k4, q, kt, vt)
+    _check_attention(q, vals[0], kt, vt, lens, H, Dh, out, lse, dtype == B.QI21_DTYPE_BF16)
+    n = B.qi21_kv4_workspace_bytes(cfg, 2, N, P, 0)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(2, H, P, device="cuda")
+    B.check("scores", B.qi21_kv4_scores(cfg, k4, 0, q, 2, N, lse, None, sc, ws, n, _stream()))
+    qn = _np(q).reshape(2, N, H, Dh)
+    want = np.zeros((2, H, P))
+    for b in range(2):
+        m = P if lens is None else lens[b]
+        for h in range(H):
+            x = qn[b, :, h] @ vals[0, 0, b, h, :m].T / np.sqrt(Dh)
+            want[b, h, :m] = np.exp(x - _np(lse)[h, b][:, None]).sum(0)
+    assert rel_l2(_np(sc), want) < 1e-5
+    keep = max(1, P // 3)
+    small = torch.full((B.qi21_kv4_cache_bytes(cfg, 2, keep),), 0x77, dtype=torch.uint8, device="cuda")
+    lo = None if lens is None else torch.zeros(4, dtype=torch.int32, device="cuda")
+    s4 = B.qi21_kv4_cache_init(small, cfg, 2, keep, lo)
+    kept = torch.zeros(1, 2, H, keep, dtype=torch.int32, device="cuda")
+    assert B.qi21_kv4_evict(cfg, k4, sc, keep, 0, s4, kept, _stream()) == B.QI21_OK
+    rows = _kv4.evict(sc.cpu().numpy()[None], lens, keep, 0)
+    assert np.array_equal(kept.cpu().numpy(), rows)
+    got = _kv4.read_values(small, 1, 2, H, keep, Dh)
+    for b in range(2):
+        m = keep if lens is None else min(keep, lens[b])
+        for h in range(H):
+            assert np.array_equal(got[0, :, b, h, :m], vals[0, :, b, h][:, rows[0, b, h, :m]])
+
+
+@pytest.mark.parametrize("mode", MODES, indirect=True)
+@pytest.mark.parametrize("N,Bn,P", [(1, 1, 700), (9, 1, 700), (60, 1, 700), (200, 1, 900), (1030, 5, 130)])
+def test_nan_reaches_exactly_its_results(B, mode, N, Bn, P):
+    """A group that is not finite makes NaNs of the results it is part of: a key of a
+    head the whole head (of its item), a value its 32 dims; a NaN query its row. And
+    an infinite key in a row that does not exist nothing at all."""
+    dtype, tdt = mode
+    H, Dh = 16, 64
+    cfg = _cfg(B, dtype, H, Dh)
+    rng = np.random.default_rng(N)
+    lens = [P - 3] * Bn
+    buf, _ = _kv4.make_buffer(rng, B, cfg, Bn, P, lens, fill=0x7F)
+    codes, scales = _kv4.buffer_views(buf, 1, Bn, H, P, Dh)
+    scales[0, 0, 0, 2, P - 9, 1] = float("nan")              # key: head 2 of item 0
+    scales[0, 1, 0, 5, 77, 0] = float("nan")                 # value: dims 0..31 of head 5
+    lt = _lens_t(lens)
+    k4 = B.qi21_kv4_cache_init(buf, cfg, Bn, P, lt)
+    k4.state = B.QI21_CACHE_EXTRACTED
+    q = torch.randn(Bn, N, H * Dh, device="cuda").to(tdt)
+    q[-1, N - 1, 9 * Dh] = float("nan")                      # query: last row of head 9, last item
+    kt, vt = (torch.randn(Bn, 40, H * Dh, device="cuda").to(tdt) for _ in range(2))
+    out, lse = _run_attention(B, cfg, k4, q, kt, vt)
+    want = torch.zeros(Bn, N, H, Dh, dtype=torch.bool, device="cuda")
+    want[0, :, 2] = True
+    want[0, :, 5, :32] = True
+    want[-1, N - 1, 9] = True
+    assert torch.equal(out.isnan().view(Bn, N, H, Dh), want)
+    wl = torch.zeros(H, Bn, N, dtype=torch.bool, device="cuda")
+    wl[2, 0] = True
+    wl[9, -1, N - 1] = True
+    assert torch.equal(lse.isnan(), wl)
+    assert not out.isinf().any() and not lse.isinf().any()
+    # the weights: NaN for the head that has a NaN query (or lse), elsewhere finite
+    n = B.qi21_kv4_workspace_bytes(cfg, Bn, N, P, 0)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(Bn, H, P, device="cuda")
+    B.check("scores", B.qi21_kv4_scores(cfg, k4, 0, q, Bn, N, lse, None, sc, ws, n, _stream()))
+    ws_want = torch.zeros(Bn, H, P, dtype=torch.bool, device="cuda")
+    ws_want[0, 2, : P - 3] = True
+    ws_want[-1, 9, : P - 3] = True
+    assert torch.equal(sc.isnan(), ws_want)
+
+
 # ------------------------------------------------------------------ scores
 
 SC = [
