@@ -1005,7 +1005,7 @@ extern "C" qi21_status qi21_kv4_attention(const qi21_config *c, const qi21_kv4_c
     if (layer < 0 || layer >= c->n_layers || !al16(q) || !al16(out) || ((uintptr_t)lse & 15) || !al16(ws) ||
         (n_tail > 0 && (!al16(k_tail) || !al16(v_tail))))
         return QI21_ERR_INVALID_ARG;
-    if (ws_bytes < kv4_plan(*c, B, B, n_q, cache->n_prefix, n_tail).total) return QI21_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < kv4_plan(*c, cache->batch, B, n_q, cache->n_prefix, n_tail).total) return QI21_ERR_WORKSPACE_TOO_SMALL;
     Launcher L((cudaStream_t)stream);
     if (c->dtype == QI21_DTYPE_BF16)
         launch_kv4_attention<bf16>(L, *c, *cache, layer, q, B, n_q, k_tail, v_tail, n_tail, out, lse, (char *)ws,

@@ -98,7 +98,7 @@ inline WsLayout ws_layout(const qi21_config &c, int64_t B, int64_t P, int64_t N)
 // Plan of an attention over a 4-bit cache: which kernel, how the work is cut, and
 // the fp32 partial results (log2-sum-exp, then normalised outputs) in the
 // workspace. Host arithmetic on sizes alone, so that the size query and the call
-// agree; 148 is the number of SMs the cuts are made for, not one they need.
+// agree (items: those of the cache, B or 1); 148 is the number of SMs the cuts are made for, not one they need.
 //   Kv4Work: the tensor-core kernel's steps. A step is one 128-key tile of one unit
 //   (item, head, unit_rows query rows); `units` units of `tiles` steps each, laid
 //   end to end, are shared out over `grid` CTAs: evenly, or (whole = 1) in whole
@@ -115,7 +115,7 @@ struct Kv4Plan {
     bool tc, expanded, rows, cluster, ok;
     int n_split;                 // rows and CUDA-core kernels: parts the keys are split into
     Kv4Work w;
-    size_t err, part_l, part_o, expand, total;
+    size_t part_l, part_o, expand, total;
 };
 
 constexpr int KV4_SMS = 148;
@@ -123,23 +123,20 @@ constexpr int KV4_SMS = 148;
 // 1 us each); whole units are taken where the even share is not that much shorter.
 constexpr int KV4_CUT_STEPS = 4;
 
-// From this many query rows on, where the 128-row query tiles fill the SMs, the
-// prefix is expanded once instead of once for every 256 rows. us, expanded / not (32
-// heads of 128, P 4608, as many tail keys as rows): 4096 rows 462 / 655, 2048 rows
-// 205 / 294, 1024 rows 117 / 153, 512 rows 103 / 89; P 33792: 1024 rows 620 / 645,
-// 512 rows 352 / 331.
-#ifndef KV4_EXPAND_ROWS
-#define KV4_EXPAND_ROWS 1024
-#endif
-constexpr int KV4_EXPAND_WAVES = 1;
-// Up to this many query rows the few-rows kernel.
-#ifndef KV4_ROWS_MAX
-#define KV4_ROWS_MAX 32
-#endif
+// The prefix is expanded once, instead of for every 256 rows, from KV4_EXPAND_ROWS
+// query rows on, where the 128-row query tiles fill the SMs, the prefix is no less than
+// the tail, and its bf16 copy stays in L2 (else from twice the rows on). us, expanded /
+// not, 32 heads of 128, as many tail keys as rows: P 4608: 4096 rows 459 / 530, 2048
+// rows 200 / 232, 1024 rows 97 / 120, 512 rows 69 / 69; P 33792 (553 MB): 2048 rows 1161
+// / 1166, 1024 rows 628 / 559. 8 x 16 heads of 64, P 512: 2048 rows 310 / 286.
+constexpr int KV4_EXPAND_ROWS = 1024;
+constexpr int64_t KV4_EXPAND_L2 = 96 << 20;     // of 126 MB
+// Up to this many query rows the few-rows kernels. us, 32 heads of 128, P 33792:
+// attention 16 rows 62, 32 rows 111, the tensor-core kernel 105 at 32 and 64 rows (but
+// 15 against 8 at 32 rows over 1032 keys of 16 heads of 64); weights 16 rows 46, 32 rows 76, the tensor-core kernel 129 at 33.
+constexpr int KV4_ROWS_MAX = 32;
 // Key splits that a cluster merges: the portable cluster size.
-#ifndef KV4_ROWS_CLUSTER
-#define KV4_ROWS_CLUSTER 8
-#endif
+constexpr int KV4_ROWS_CLUSTER = 8;
 
 inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
     Kv4Plan p{};
@@ -177,7 +174,9 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t 
         p.w.unit_rows = (int)ur;
         p.w.slot_rows = (int)(qt == 1 ? n_q : ur);
         if (units > INT32_MAX) p.ok = false;
-        p.expanded = n_q >= KV4_EXPAND_ROWS && B * H * ((n_q + 127) / 128) >= KV4_EXPAND_WAVES * KV4_SMS;
+        const int64_t copy = 4 * items * tp * 128 * c.d_model;
+        p.expanded = n_q >= (copy <= KV4_EXPAND_L2 ? 1 : 2) * KV4_EXPAND_ROWS && P >= n_tail &&
+                     B * H * ((n_q + 127) / 128) >= KV4_SMS;
         if (p.expanded && (B > 65535 || (n_q + 127) / 128 > INT32_MAX)) p.ok = false;
         rows = p.w.whole || p.expanded ? 0 : (size_t)2 * p.w.grid * p.w.slot_rows;
     } else {
@@ -233,12 +232,17 @@ inline Kv4ScorePlan kv4_score_plan(const qi21_config &c, int64_t items, int64_t 
     return p;
 }
 
-// Workspace of the attention, and of the weights over a cache of B items or of one.
+// Workspace of the attention and of the weights, over a cache of B items or of one
+// that B requests share.
 inline size_t kv4_ops_workspace(const qi21_config &c, int64_t B, int64_t n_q, int64_t P, int64_t n_tail) {
-    size_t n = kv4_plan(c, B, B, n_q, P, n_tail).total;
-    const size_t a = kv4_score_plan(c, B, n_q, P).total, one = kv4_score_plan(c, 1, B * n_q, P).total;
-    if (n < a) n = a;
-    return n < one ? one : n;
+    size_t most = 0;
+    for (int64_t items = 1; items <= B; items += B > 1 ? B - 1 : 1) {
+        const size_t a = kv4_plan(c, items, B, n_q, P, n_tail).total;
+        const size_t s = kv4_score_plan(c, items, items == 1 ? B * n_q : n_q, P).total;
+        most = most > a ? most : a;
+        most = most > s ? most : s;
+    }
+    return most;
 }
 
 // Workspace of the cached step over a 4-bit cache: that of a cached step without

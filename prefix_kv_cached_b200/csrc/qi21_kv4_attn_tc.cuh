@@ -24,6 +24,10 @@
 //                      operand layout. Tail tiles: TMA loads into the same ring.
 //   warp 12          : TMEM allocator + UMMA issuer
 //   warp 13, 14      : bulk copies of codes and scales into the staging ring; Q loads
+// Bound by the expansion (four warps, 860 cycles a tile alone, twice that beside the
+// softmax) and the chain of the softmax: 145 us for 256 rows over P 33792, 32 heads of
+// 128 (980 TFLOP/s), 69 us for 512 rows over 4608 + 512 keys; two producer warps instead
+// of four (and 168 registers for all) 297 us for the former.
 // Registers: 512 threads launched with 128 each; the softmax warpgroups (128
 // scores a row in registers) take 192 each, the producers 72, the last 56
 // (192 + 192 + 72 + 56 = 4 x 128).

@@ -21,7 +21,10 @@
 // cluster (else by k_kv4_combine), in a fixed order.
 // (tcgen05 would want the expanded cache in shared memory: 2 bytes an element
 // written and read again, which alone is as long as the read of 4.5 bits from HBM.)
-// Bound by HBM; next the ALU pipe, about 1.4 operations an element at half rate.
+// Bound by the expansion's instructions (337 for 16 keys of K and V at head_dim 128,
+// 159 of them on the ALU pipe at half rate): 50 us for one row over P 33792, 32 heads of
+// 128 (3.1 TB/s), of which the pass over the key splits' results takes some 8; the loads
+// alone run 29 us, HBM's own time is 24.
 #pragma once
 #include "qi21_kv4_attn_tc.cuh"
 

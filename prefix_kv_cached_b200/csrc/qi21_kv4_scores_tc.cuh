@@ -17,15 +17,17 @@
 //   warp 9     : Q tiles by TMA and the queries' offsets -lse2
 // Bound by the exponentials: 128 x 128 a tile take 1024 cycles of the SM's MUFU
 // units, the product 512 tensor cycles (head_dim 128). KV4_SC_POLY of every 8 pairs
-// therefore go to the FMA pipe.
+// therefore go to the FMA pipe. 164 us for 4096 queries, P 4608, 32 heads of 128 (940
+// TFLOP/s); with the exponentials and sums left out it runs 104 us, the product's own
+// time. One warpgroup of exponentials a CTA is as fast as the two here take with twice
+// the rows in registers; loading S one key a thread (its 128 queries' offsets from
+// shared memory) costs 27 us more.
 #pragma once
 #include "qi21_kv4_attn_tc.cuh"
 
 namespace qi21 {
 
-#ifndef KV4_SC_POLY
-#define KV4_SC_POLY 2
-#endif
+constexpr int KV4_SC_POLY = 2;   // us at the size above with 0 .. 3 of 8: 182, 170, 165, 173
 
 template <int DH>
 struct Kv4ScoreCfg {
@@ -45,8 +47,8 @@ struct Kv4ScoreTcArgs {
     float *part;                 // [n_split][B][H][Pp] when n_split > 1
 };
 
-// 2^x of a pair by a polynomial of degree 5 (2e-7) as in ex2_poly2_deg, with 2^n as a
-// factor: a NaN stays one, x > 128 gives +inf, x < -127 gives 0.
+// 2^x of a pair by a polynomial of degree 5 (exp2_poly_fit.py's fit of that degree,
+// relative error 2e-7: these weights are a result in fp32), with 2^n as a factor: a NaN stays one, x > 128 gives +inf, x < -127 gives 0.
 __device__ __forceinline__ uint64_t kv4_ex2_pair(uint64_t x2) {
     float x0, x1;
     f2_unpack(x2, x0, x1);

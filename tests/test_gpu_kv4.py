@@ -202,15 +202,17 @@ ATT = [
 ]
 
 
-def _run_attention(B, cfg, k4, q, kt, vt, lse=True, ws=None, layer=0):
+def _run_attention(B, cfg, k4, q, kt, vt, lse=True, layer=0):
     Bn, N, H = q.shape[0], q.shape[1], cfg.n_heads
     T = 0 if kt is None else kt.shape[1]
     n = B.qi21_kv4_workspace_bytes(cfg, Bn, N, k4.n_prefix, T)
-    ws = torch.zeros(n, dtype=torch.uint8, device="cuda") if ws is None else ws
+    ws = torch.full((n + 1024,), 0x5C, dtype=torch.uint8, device="cuda")
+    ws[:64] = 0                                             # the error words
     out = torch.full_like(q, float("nan"))
     ls = torch.full((H, Bn, N), float("nan"), device="cuda") if lse else None
     B.check("attention", B.qi21_kv4_attention(cfg, k4, layer, q, Bn, N, kt, vt, T, out, ls, ws, n, _stream()))
     B.check("device", B.qi21_check_device_error(ws, n, _stream()))
+    assert (ws[n:] == 0x5C).all()
     return out, ls
 
 
@@ -295,6 +297,37 @@ def test_attention_scores_of_very_different_size(B, mode, N):
         tol = (FP32_REL + 2 * ds) * mag + (HALF * (mag + np.abs(o)) if dtype == B.QI21_DTYPE_BF16 else 0)
         assert (np.abs(_np(out).reshape(N, 2, 128)[:, h] - o) <= tol).all()
         assert np.abs(_np(lse)[h, 0] - ls).max() <= LSE_ABS + ds
+
+
+def test_workspace_of_a_shared_and_of_an_own_prefix(B):
+    """Sizes at which five items of their own and one shared by five take different
+    kernels: the queried workspace holds either (the bytes behind it stay), and both
+    give the same results to the rounding of weights and results."""
+    H, Dh, Bn, P, N = 16, 64, 5, 6000, 1100
+    cfg = _cfg(B, B.QI21_DTYPE_BF16, H, Dh)
+    rng = np.random.default_rng(1)
+    one, _ = _kv4.make_buffer(rng, B, cfg, 1, P)
+    many = torch.zeros(B.qi21_kv4_cache_bytes(cfg, Bn, P), dtype=torch.uint8, device="cuda")
+    for dst, src in zip(_kv4.buffer_views(many, 1, Bn, H, P, Dh), _kv4.buffer_views(one, 1, 1, H, P, Dh)):
+        dst.copy_(src.expand_as(dst))
+    q = torch.randn(Bn, N, H * Dh, device="cuda").bfloat16()
+    n = B.qi21_kv4_workspace_bytes(cfg, Bn, N, P, 0)
+    ws = torch.full((n + 4096,), 0x5C, dtype=torch.uint8, device="cuda")
+    ws[:64] = 0
+    outs = []
+    for buf, items in ((one, 1), (many, Bn)):
+        k4 = B.qi21_kv4_cache_init(buf, cfg, items, P)
+        k4.state = B.QI21_CACHE_EXTRACTED
+        out, lse = torch.empty_like(q), torch.empty(H, Bn, N, device="cuda")
+        sc = torch.empty(items, H, P, device="cuda")
+        B.check("a", B.qi21_kv4_attention(cfg, k4, 0, q, Bn, N, None, None, 0, out, lse, ws, n, _stream()))
+        B.check("s", B.qi21_kv4_scores(cfg, k4, 0, q, Bn, N, lse, None, sc, ws, n, _stream()))
+        B.check("d", B.qi21_check_device_error(ws, n, _stream()))
+        outs.append((out, lse, sc.sum(0)))
+    assert (ws[n:] == 0x5C).all()
+    a, b = outs
+    assert rel_l2(_np(a[0]), _np(b[0])) < 2 * HALF and rel_l2(_np(a[1]), _np(b[1])) < 1e-5
+    assert rel_l2(_np(a[2]), _np(b[2])) < 3e-5
 
 
 @pytest.mark.parametrize("mode", ["f32", "bf16_cuda_cores"], indirect=True)
