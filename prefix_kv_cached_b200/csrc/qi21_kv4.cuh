@@ -337,6 +337,48 @@ __device__ __forceinline__ uint32_t kv4_rank(float s, int j, int n_protected) {
 }
 
 
+constexpr int KV4_GATHER = 4;    // rows of a thread
+
+// Copy rows of K and V into the smaller cache: THREADS threads, those of the kept list
+// from r0 on, four a thread. A thread moves one group (16 bytes of codes and its scale)
+// of its rows, all of them in flight at once. Bound by HBM's latency and its 64-byte
+// pieces: 38 us for 170 MB (8 layers, 32 heads of 128, 2304 of 4608 rows).
+template <int THREADS>
+__device__ __forceinline__ void kv4_gather_rows(const uint8_t *src, const Kv4Dims &c, const int *list, int keep, int r0,
+                                                int l, int b, int h, uint8_t *dst, const Kv4Dims &o) {
+    const uint32_t G = c.Dh / KV4_GROUP, rows = THREADS / G;   // G threads a row, `rows` rows at a time
+    const uint32_t t = threadIdx.x / G, g = threadIdx.x - t * G;
+    if (t >= rows) return;                                     // THREADS is no multiple of 3
+    int j[KV4_GATHER];
+#pragma unroll
+    for (int i = 0; i < KV4_GATHER; ++i) {
+        const int r = r0 + t + i * rows;
+        j[i] = r < keep ? list[r] : -1;
+    }
+    const uint16_t *from_s = reinterpret_cast<const uint16_t *>(src + c.scales_off);
+    uint16_t *to_s = reinterpret_cast<uint16_t *>(dst + o.scales_off);
+    uint4 code[2][KV4_GATHER];
+    uint16_t scale[2][KV4_GATHER];
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int i = 0; i < KV4_GATHER; ++i)
+            if (j[i] >= 0) {
+                const int64_t from = (kv4_row0(c, l, which, b, h) + j[i]) * G + g;
+                code[which][i] = reinterpret_cast<const uint4 *>(src)[from];
+                scale[which][i] = from_s[from];
+            }
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int i = 0; i < KV4_GATHER; ++i)
+            if (j[i] >= 0) {
+                const int64_t to = (kv4_row0(o, l, which, b, h) + r0 + t + i * rows) * G + g;
+                reinterpret_cast<uint4 *>(dst)[to] = code[which][i];
+                to_s[to] = scale[which][i];
+            }
+}
+
 // The rows that one (layer, item, head) keeps: the `keep` largest of its ranks,
 // ties to the lowest row, in ascending order; -1 behind them where the item has
 // fewer rows. Radix selection, 8 bits a pass from the top, on integers: exact, and
@@ -344,11 +386,12 @@ __device__ __forceinline__ uint32_t kv4_rank(float s, int j, int n_protected) {
 // so that one scan over the block gives every row its place; where the rows are more
 // than THREADS x IPT, they are read again tile by tile in each pass. Bound by latency
 // (barriers and one read of the scores): 10 us for 1024 heads of 512 rows, 18 us for
-// 256 of 4608. grid (H, B, L).
-template <int THREADS, int IPT>
+// 256 of 4608. GATHER: the block then copies the rows it has chosen, which runs under the
+// selections of the blocks beside it. grid (H, B, L).
+template <int THREADS, int IPT, bool GATHER>
 __global__ void __launch_bounds__(THREADS)
-    k_kv4_select(const float *scores, Kv4Dims c, const int *prefix_len, int keep,
-                 int n_protected, int *kept, int *dst_len) {
+    k_kv4_select(const float *scores, Kv4Dims c, const int *prefix_len, int keep, int n_protected, int *kept,
+                 int *dst_len, const uint8_t *src, uint8_t *dst, Kv4Dims o) {
     constexpr int W = THREADS / 32, TILE = THREADS * IPT;
     static_assert(TILE <= 8192, "two counts share 32 bits");
     __shared__ int hist[2][256];
@@ -371,7 +414,7 @@ __global__ void __launch_bounds__(THREADS)
             key[i] = j < len ? kv4_rank(sc[j], j, n_protected) : 0u;
         }
     };
-    load(0);
+    if (tiles == 1) load(0);
     uint32_t prefix = 0;         // the bits of the count-th largest rank found so far
     int need = count;            // how many ranks with these bits are taken
     if (count < len) {
@@ -381,12 +424,23 @@ __global__ void __launch_bounds__(THREADS)
             const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
             int *hs = hist[pass & 1];
             __syncthreads();                                   // hs is zero
-            for (int t = 0; t < tiles; ++t) {
-                if (tiles > 1) load(t);
+            if (tiles == 1) {
 #pragma unroll
                 for (int i = 0; i < IPT; ++i)
-                    if (t * TILE + tid * IPT + i < len && (key[i] & mask) == prefix)
-                        atomicAdd(&hs[(key[i] >> shift) & 255], 1);
+                    if (tid * IPT + i < len && (key[i] & mask) == prefix) atomicAdd(&hs[(key[i] >> shift) & 255], 1);
+            } else {
+                // the order does not matter here: neighbours read neighbours, 8 loads in flight
+                for (int j0 = tid; j0 < len; j0 += 8 * THREADS) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = j0 + i * THREADS < len ? sc[j0 + i * THREADS] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = j0 + i * THREADS;
+                        const uint32_t r = kv4_rank(v[i], j, n_protected);
+                        if (j < len && (r & mask) == prefix) atomicAdd(&hs[(r >> shift) & 255], 1);
+                    }
+                }
             }
             __syncthreads();
             if (wid == 0) {
@@ -466,51 +520,21 @@ __global__ void __launch_bounds__(THREADS)
         ties0 += all >> 16;
     }
     for (int i = count + tid; i < keep; i += THREADS) out[i] = -1;
+    if (GATHER) {
+        __syncthreads();                       // the list that the block has written
+        const int step = KV4_GATHER * (THREADS / (c.Dh / KV4_GROUP));
+        for (int r0 = 0; r0 < count; r0 += step) kv4_gather_rows<THREADS>(src, c, out, count, r0, l, b, h, dst, o);
+    }
 }
 
-constexpr int KV4_GATHER = 4;    // rows of a thread
-
-// Copy the kept rows of K and V into the smaller cache. A thread moves one group
-// (16 bytes of codes and its scale) of four rows of K and of V, all of them in flight
-// at once. Bound by HBM's latency and its 64-byte pieces: 38 us for 170 MB (8 layers,
-// 32 heads of 128, 2304 of 4608 rows). grid (pieces, H, L * B).
-__global__ void __launch_bounds__(256)
+// The gather by itself, for few heads with many rows each. grid (blocks of rows, H, L * B).
+static __global__ void __launch_bounds__(256)
     k_kv4_gather(const uint8_t *src, Kv4Dims c, const int *kept, int keep, uint8_t *dst, Kv4Dims o) {
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t G = c.Dh / KV4_GROUP, rows = 256 / G;       // G threads a row, `rows` rows at a time
-    const int g = threadIdx.x % G, r0 = blockIdx.x * (KV4_GATHER * rows) + threadIdx.x / G;
-    if (threadIdx.x / G >= rows) return;                       // 256 is no multiple of 3
     const int h = blockIdx.y, l = blockIdx.z / c.B, b = blockIdx.z - l * c.B;
-    const int *list = kept + (((int64_t)l * c.B + b) * c.H + h) * keep;
-    int j[KV4_GATHER];
-#pragma unroll
-    for (int i = 0; i < KV4_GATHER; ++i) {
-        const int r = r0 + i * rows;
-        j[i] = r < keep ? list[r] : -1;
-    }
-    const uint16_t *from_s = reinterpret_cast<const uint16_t *>(src + c.scales_off);
-    uint16_t *to_s = reinterpret_cast<uint16_t *>(dst + o.scales_off);
-    uint4 code[2][KV4_GATHER];
-    uint16_t scale[2][KV4_GATHER];
-#pragma unroll
-    for (int which = 0; which < 2; ++which)
-#pragma unroll
-        for (int i = 0; i < KV4_GATHER; ++i)
-            if (j[i] >= 0) {
-                const int64_t from = (kv4_row0(c, l, which, b, h) + j[i]) * G + g;
-                code[which][i] = reinterpret_cast<const uint4 *>(src)[from];
-                scale[which][i] = from_s[from];
-            }
-#pragma unroll
-    for (int which = 0; which < 2; ++which)
-#pragma unroll
-        for (int i = 0; i < KV4_GATHER; ++i)
-            if (j[i] >= 0) {
-                const int64_t to = (kv4_row0(o, l, which, b, h) + r0 + i * rows) * G + g;
-                reinterpret_cast<uint4 *>(dst)[to] = code[which][i];
-                to_s[to] = scale[which][i];
-            }
+    kv4_gather_rows<256>(src, c, kept + (((int64_t)l * c.B + b) * c.H + h) * keep, keep,
+                         blockIdx.x * (KV4_GATHER * (256 / (c.Dh / KV4_GROUP))), l, b, h, dst, o);
 }
 
 // ------------------------------------------------------------------ CUDA-core attention

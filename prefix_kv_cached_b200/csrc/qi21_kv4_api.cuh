@@ -325,19 +325,28 @@ static void launch_kv4_scores(Launcher &L, const qi21_config &c, const qi21_kv4_
     }
 }
 
+constexpr int KV4_EVICT_HEADS = KV4_SMS;
+
 static void launch_kv4_evict(Launcher &L, const qi21_config &c, const qi21_kv4_cache &src, const float *scores,
                              int keep, int n_protected, const qi21_kv4_cache &dst, int *kept) {
     const Kv4Dims cd = kv4_dims(src), od = kv4_dims(dst);
-    L.run("kv4_select", [&] {
+    // From a head an SM on, a block copies the rows of the head it has selected; fewer
+    // heads leave SMs without a copy to make, and the rows are copied by a grid of their
+    // own. us, one kernel / two: 1024 heads 512 -> 333 rows 16.5 / 19.7, 256 heads 4608 ->
+    // 2304 rows 50.7 / 51.7, 1024 heads 155.7 / 166.3; 64 heads 27.8 / 27.0.
+    const bool one = (int64_t)c.n_layers * cd.B * cd.H >= KV4_EVICT_HEADS;
+    L.run(one ? "kv4_evict" : "kv4_select", [&] {
         // rows a thread holds: as many as the prefix needs, so that it is read once
         auto go = [&](auto *kernel, int threads) {
             launch_dep(kernel, dim3(cd.H, cd.B, c.n_layers), dim3(threads), 0, L.st, nullptr, scores, cd,
-                       src.prefix_len, keep, n_protected, kept, dst.prefix_len);
+                       src.prefix_len, keep, n_protected, kept, dst.prefix_len, (const uint8_t *)src.base,
+                       (uint8_t *)dst.base, od);
         };
-        if (cd.P <= 512) go(k_kv4_select<128, 4>, 128);
-        else if (cd.P <= 2048) go(k_kv4_select<256, 8>, 256);
-        else go(k_kv4_select<512, 16>, 512);
+        if (cd.P <= 512) one ? go(k_kv4_select<128, 4, true>, 128) : go(k_kv4_select<128, 4, false>, 128);
+        else if (cd.P <= 2048) one ? go(k_kv4_select<256, 8, true>, 256) : go(k_kv4_select<256, 8, false>, 256);
+        else one ? go(k_kv4_select<512, 16, true>, 512) : go(k_kv4_select<512, 16, false>, 512);
     });
+    if (one) return;
     L.run("kv4_gather", [&] {
         const int rows = KV4_GATHER * (256 / (cd.Dh / KV4_GROUP));           // of a block
         launch_dep(k_kv4_gather, dim3((keep + rows - 1) / rows, cd.H, c.n_layers * cd.B), dim3(256), 0, L.st, nullptr,

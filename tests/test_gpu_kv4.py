@@ -542,6 +542,41 @@ def test_evict(B, H, Dh, L, Bn, P, keep, prot, lens):
         assert lens_out[:Bn].tolist() == [min(keep, n) for n in lens]
 
 
+@pytest.mark.parametrize("L,Bn,H,Dh,P,keep,prot,ragged", [
+    (5, 1, 32, 64, 8300, 4100, 7, False), (3, 2, 32, 128, 2049, 1, 0, True), (10, 1, 16, 64, 300, 299, 299, False),
+    (1, 1, 4, 64, 20000, 9999, 100, False), (4, 3, 16, 64, 1500, 800, 20, True), (2, 3, 32, 64, 512, 512, 0, True)])
+def test_evict_many_heads_and_long_prefixes(B, L, Bn, H, Dh, P, keep, prot, ragged):
+    """Either form of the eviction (one kernel, or selection and copy), prefixes that one
+    block reads in pieces, against a stable sort; the copied bytes, and no others."""
+    cfg = _cfg(B, B.QI21_DTYPE_BF16, H, Dh, L)
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    buf = torch.randint(0, 256, (B.qi21_kv4_cache_bytes(cfg, Bn, P),), dtype=torch.uint8, device="cuda", generator=gen)
+    lens = torch.randint(0, P + 1, (4,), dtype=torch.int32, device="cuda", generator=gen) if ragged else None
+    k4 = B.qi21_kv4_cache_init(buf, cfg, Bn, P, lens)
+    k4.state = B.QI21_CACHE_EXTRACTED
+    sc = torch.randn(L, Bn, H, P, device="cuda", generator=gen).mul(3).round()          # ties everywhere
+    out = torch.full((B.qi21_kv4_cache_bytes(cfg, Bn, keep),), 0x77, dtype=torch.uint8, device="cuda")
+    lens_out = torch.zeros(4, dtype=torch.int32, device="cuda")
+    small = B.qi21_kv4_cache_init(out, cfg, Bn, keep, lens_out)
+    kept = torch.full((L, Bn, H, keep), 7, dtype=torch.int32, device="cuda")
+    assert B.qi21_kv4_evict(cfg, k4, sc, keep, prot, small, kept, _stream()) == B.QI21_OK
+    c0, s0 = _kv4.buffer_views(buf, L, Bn, H, P, Dh)
+    c1, s1 = _kv4.buffer_views(out, L, Bn, H, keep, Dh)
+    s0, s1 = s0.view(torch.int16), s1.view(torch.int16)
+    for b in range(Bn):
+        n = int(lens[b]) if ragged else P
+        m = min(keep, n)
+        rank = sc[:, b, :, :n].clone()
+        rank[..., : min(prot, n)] = float("inf")
+        want = torch.sort(rank, dim=-1, descending=True, stable=True).indices[..., :m].sort(-1).values
+        assert torch.equal(kept[:, b, :, :m].long(), want) and (kept[:, b, :, m:] == -1).all()
+        assert int(lens_out[b]) == m
+        at = want[:, None, :, :, None].expand(L, 2, H, m, 1)
+        assert torch.equal(c1[:, :, b, :, :m], c0[:, :, b].gather(3, at.expand(-1, -1, -1, -1, Dh // 2)))
+        assert torch.equal(s1[:, :, b, :, :m], s0[:, :, b].gather(3, at.expand(-1, -1, -1, -1, Dh // 32)))
+        assert (c1[:, :, b, :, m:] == 0x77).all() and (s1[:, :, b, :, m:] == 0x7777).all()
+
+
 # ------------------------------------------------------------------ the cached step over the 4-bit prefix
 
 def _inputs(w):
