@@ -256,7 +256,8 @@ size_t qi21_kv4_cache_bytes(const qi21_config *cfg, int32_t batch, int32_t n_pre
 qi21_status qi21_kv4_cache_init(qi21_kv4_cache *cache, void *base, const qi21_config *cfg,
                                 int32_t batch, int32_t n_prefix, int32_t *prefix_len);
 /* Workspace of qi21_kv4_attention and qi21_kv4_scores for these sizes (n_tail = 0
- * for the scores), and of qi21_cached_step_kv4. */
+ * for the scores), and of qi21_cached_step_kv4. Not monotone in n_prefix: the step
+ * over a prefix that qi21_kv4_evict has shortened can need more. */
 size_t qi21_kv4_workspace_bytes(const qi21_config *cfg, int32_t batch, int32_t n_q,
                                 int32_t n_prefix, int32_t n_tail);
 size_t qi21_kv4_step_workspace_bytes(const qi21_config *cfg, int32_t batch, int32_t n_prefix,

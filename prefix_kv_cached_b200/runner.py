@@ -145,9 +145,11 @@ class Qi21Runner:
         self.kv4 = B.qi21_kv4_cache_init(self.kv4_buf, self.cfg, nb, self.P)
         B.check("qi21_kv4_quantize", B.qi21_kv4_quantize(self.cfg, self.cache, self.kv4, self.stream))
         self.kv4_scores: Optional[torch.Tensor] = None
-        # the whole prefix needs the largest workspace
-        self.kv4_ws = torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, self.P, self.N),
-                                  dtype=torch.uint8, device=self.device)
+        self.kv4_ws = self._kv4_workspace(self.P)
+
+    def _kv4_workspace(self, n_prefix: int) -> torch.Tensor:
+        return torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, n_prefix, self.N), dtype=torch.uint8,
+                           device=self.device)
 
     def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
         """The cached step over the 4-bit prefix. accumulate: add every layer's
@@ -171,10 +173,14 @@ class Qi21Runner:
         k = self.kv4
         buf = torch.empty(B.qi21_kv4_cache_bytes(self.cfg, k.batch, keep), dtype=torch.uint8, device=self.device)
         small = B.qi21_kv4_cache_init(buf, self.cfg, k.batch, keep)
+        # fewer rows can need more workspace: other splits of the work, other kernels
+        need = B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, keep, self.N)
+        ws = self.kv4_ws if self.kv4_ws.numel() >= need else self._kv4_workspace(keep)
         kept = torch.empty(k.n_layers, k.batch, k.n_heads, keep, dtype=torch.int32, device=self.device)
         B.check("qi21_kv4_evict", B.qi21_kv4_evict(self.cfg, k, self.kv4_scores, keep, n_protected, small, kept,
                                                    self.stream))
         self.kv4, self.kv4_buf, self.kv4_scores = small, buf, None
+        self.kv4_ws = ws
         return kept
 
     def denoise_kv4(self, prefix_hidden: torch.Tensor, x0: torch.Tensor, sigmas=None, keep: Optional[int] = None,

@@ -1,0 +1,58 @@
+"""What Qi21Runner does on the host around the 4-bit cache's calls: the buffers it
+holds, without a GPU. The library's launches are replaced; its size queries and
+argument checks are the real ones."""
+import pytest
+import torch
+
+from qi21_synth import configs as C
+
+H32 = C.ModelShape(4096, 32, 128, 1, 8192, 64, 256)
+H16 = C.ModelShape(1024, 16, 64, 1, 2048, 64, 256)
+
+
+@pytest.fixture
+def B(monkeypatch):
+    from prefix_kv_cached_b200 import build
+    build.build()
+    from prefix_kv_cached_b200 import binding, runner
+
+    def extracted(cache4):
+        cache4.state = binding.QI21_CACHE_EXTRACTED
+        return binding.QI21_OK
+
+    monkeypatch.setattr(binding, "qi21_kv4_quantize", lambda cfg, src, dst, stream=0: extracted(dst))
+    monkeypatch.setattr(binding, "qi21_kv4_evict",
+                        lambda cfg, src, scores, keep, prot, dst, kept, stream=0: extracted(dst))
+    monkeypatch.setattr(runner.Qi21Runner, "stream", 0)
+    return binding
+
+
+def _runner(B, shape, batch, P, N, shared=False):
+    """A runner as its constructor leaves it, without weights or a GPU."""
+    from prefix_kv_cached_b200.runner import Qi21Runner, make_config
+    r = object.__new__(Qi21Runner)
+    r.device, r.cfg = torch.device("cpu"), make_config(shape, B.QI21_DTYPE_BF16)
+    r.Bn, r.P, r.N, r.shared_prefix, r.cache = batch, P, N, shared, None
+    return r
+
+
+def _evict(r, keep):
+    k = r.kv4
+    r.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix)
+    r.evict_prefix(keep)
+
+
+# the first three, the fourth's queries and the last one's partial results grow as the prefix shrinks
+@pytest.mark.parametrize("shape,batch,P,N,keeps", [
+    (H32, 1, 8192, 1024, (4096,)), (H32, 1, 6400, 1024, (4800, 1000, 1)), (H32, 1, 12000, 1100, (6000,)),
+    (H16, 4, 1159, 512, (565, 3)), (C.MID, 8, 512, 256, (511, 333, 256, 100, 1)), (H16, 1, 4096, 4096, (2048,)),
+    (C.SMALL, 2, 198, 300, (99, 1)), (H32, 1, 4608, 4096, (4607, 2304, 1))])
+@pytest.mark.parametrize("shared", [False, True])
+def test_workspace_holds_the_step_after_every_eviction(B, shape, batch, P, N, keeps, shared):
+    r = _runner(B, shape, batch, P, N, shared)
+    r.quantise_prefix()
+    assert r.kv4_ws.numel() >= B.qi21_kv4_step_workspace_bytes(r.cfg, batch, P, N)
+    for keep in keeps:
+        _evict(r, keep)
+        assert r.kv4.n_prefix == keep
+        assert r.kv4_ws.numel() >= B.qi21_kv4_step_workspace_bytes(r.cfg, batch, keep, N), keep
