@@ -151,6 +151,16 @@ class Qi21Runner:
         return torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, n_prefix, self.N), dtype=torch.uint8,
                            device=self.device)
 
+    def _kv4_in_use(self):
+        """The current stream has work on the 4-bit buffers. Later calls, on whatever
+        stream, drop them; the allocator must not give their memory to the stream they
+        were allocated on before this work is done."""
+        if self.device.type == "cuda":
+            s = torch.cuda.current_stream(self.device)
+            for t in (self.kv4_buf, self.kv4_ws, self.kv4_scores):
+                if t is not None:
+                    t.record_stream(s)
+
     def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
         """The cached step over the 4-bit prefix. accumulate: add every layer's
         attention weights of this step to kv4_scores [L][items][H][rows]."""
@@ -158,6 +168,7 @@ class Qi21Runner:
             k = self.kv4
             self.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix, dtype=torch.float32,
                                           device=self.device)
+        self._kv4_in_use()
         B.check("qi21_cached_step_kv4", B.qi21_cached_step_kv4(
             self.cfg, self.wstruct, self.kv4, self.Bn, self.N, x, self.cos_sin_target, self.mod_target,
             self.scale_final, v_out, self.kv4_scores if accumulate else None, self.kv4_ws, self.kv4_ws.numel(),
@@ -177,6 +188,7 @@ class Qi21Runner:
         need = B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, keep, self.N)
         ws = self.kv4_ws if self.kv4_ws.numel() >= need else self._kv4_workspace(keep)
         kept = torch.empty(k.n_layers, k.batch, k.n_heads, keep, dtype=torch.int32, device=self.device)
+        self._kv4_in_use()
         B.check("qi21_kv4_evict", B.qi21_kv4_evict(self.cfg, k, self.kv4_scores, keep, n_protected, small, kept,
                                                    self.stream))
         self.kv4, self.kv4_buf, self.kv4_scores = small, buf, None

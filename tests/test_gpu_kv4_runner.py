@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from qi21_synth import configs as C
+from tests import _kv4
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,66 @@ def test_image_goes_on_after_an_eviction_that_needs_more_workspace(B, mid):
     x = mid.denoise_kv4(pre, x0, mid.w.sigmas[:4], keep=333, n_protected=256)
     B.check("device", B.qi21_check_device_error(mid.kv4_ws, mid.kv4_ws.numel(), mid.stream))
     assert mid.kv4.n_prefix == 333 and mid.kv4_ws.numel() >= need[1] and x.isfinite().all()
+
+
+WAIT = 400_000_000          # cycles that a stream is held up for: some 0.2 s
+
+
+def _quantised(r, pre):
+    r.set_prefix_row()
+    r.prefix_extract(pre)
+    r.quantise_prefix()
+    r.set_target_row(r.w.sigmas[0])
+
+
+def test_eviction_on_another_stream_keeps_what_it_reads(B, mid):
+    """The buffers that an eviction drops belong to the stream they were allocated on.
+    While the eviction waits on another one, that stream's next allocations must not
+    be given their memory."""
+    r, keep = mid, 100
+    pre, x0 = _inputs(r, 1)
+    v = torch.empty_like(x0)
+    _quantised(r, pre)
+    r.cached_step_kv4(x0, v, accumulate=True)
+    torch.cuda.synchronize()
+    old = [(t.data_ptr(), t.numel() * t.element_size()) for t in (r.kv4_buf, r.kv4_scores)]
+    L, H, Dh = r.cfg.n_layers, r.cfg.n_heads, r.cfg.head_dim
+    vals = _kv4.read_values(r.kv4_buf, L, r.Bn, H, r.P, Dh)
+    rows = _kv4.evict(r.kv4_scores.cpu().numpy(), None, keep, 7)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(WAIT)
+        kept = r.evict_prefix(keep, 7)
+    taken = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for _, n in old for _ in range(2)]
+    assert not side.query()                               # the eviction has not run yet
+    for t in taken:
+        assert all(t.data_ptr() + t.numel() <= p or p + n <= t.data_ptr() for p, n in old)
+    torch.cuda.synchronize()
+    assert (kept.cpu().numpy() == rows).all()
+    got = _kv4.read_values(r.kv4_buf, L, r.Bn, H, keep, Dh)
+    for l, b, h in ((0, 0, 0), (L - 1, r.Bn - 1, H - 1), (3, 5, 7)):
+        assert (got[l, :, b, h] == vals[l, :, b, h][:, rows[l, b, h]]).all()
+
+
+def test_requantising_under_a_step_on_another_stream(B, mid):
+    """quantise_prefix replaces the 4-bit cache and its workspace; a step on another
+    stream that still reads the ones before gives what it gives alone."""
+    r = mid
+    pre, x0 = _inputs(r, 2)
+    want, v = torch.empty_like(x0), torch.empty_like(x0)
+    _quantised(r, pre)
+    r.cached_step_kv4(x0, want)
+    torch.cuda.synchronize()
+    old = [(t.data_ptr(), t.numel()) for t in (r.kv4_buf, r.kv4_ws)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(WAIT)
+        r.cached_step_kv4(x0, v)
+    r.quantise_prefix()
+    taken = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for _, n in old for _ in range(2)]
+    assert not side.query()
+    for t in [r.kv4_buf, r.kv4_ws] + taken:
+        assert all(t.data_ptr() + t.numel() <= p or p + n <= t.data_ptr() for p, n in old)
+    torch.cuda.synchronize()
+    # bf16: the GEMMs add their last partial tiles in no fixed order
+    assert (v - want).norm() < 1e-2 * want.norm()
