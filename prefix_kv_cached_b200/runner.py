@@ -93,6 +93,11 @@ class Qi21Runner:
         self.mod_target = torch.zeros_like(self.mod_prefix)
         self.scale_final = torch.zeros(sh.d_model, dtype=torch.float32, device=self.device)
         self._sf0 = torch.zeros_like(self.scale_final)
+        # the 4-bit prefix cache (quantise_prefix)
+        self.kv4: Optional[B.qi21_kv4_cache] = None
+        self.kv4_buf: Optional[torch.Tensor] = None
+        self.kv4_scores: Optional[torch.Tensor] = None
+        self.kv4_ws: Optional[torch.Tensor] = None
 
     @property
     def stream(self) -> int:
@@ -140,12 +145,11 @@ class Qi21Runner:
         """Hold the extracted prefix in 4 bits from here on (for cached_step_kv4);
         the cache buffer itself is kept for the next extract."""
         nb = 1 if self.shared_prefix else self.Bn
-        self.kv4_buf = torch.empty(B.qi21_kv4_cache_bytes(self.cfg, nb, self.P), dtype=torch.uint8,
-                                   device=self.device)
-        self.kv4 = B.qi21_kv4_cache_init(self.kv4_buf, self.cfg, nb, self.P)
-        B.check("qi21_kv4_quantize", B.qi21_kv4_quantize(self.cfg, self.cache, self.kv4, self.stream))
-        self.kv4_scores: Optional[torch.Tensor] = None
-        self.kv4_ws = self._kv4_workspace(self.P)
+        buf = torch.empty(B.qi21_kv4_cache_bytes(self.cfg, nb, self.P), dtype=torch.uint8, device=self.device)
+        cache4 = B.qi21_kv4_cache_init(buf, self.cfg, nb, self.P)
+        ws = self._kv4_workspace(self.P)
+        B.check("qi21_kv4_quantize", B.qi21_kv4_quantize(self.cfg, self.cache, cache4, self.stream))
+        self.kv4, self.kv4_buf, self.kv4_scores, self.kv4_ws = cache4, buf, None, ws
 
     def _kv4_workspace(self, n_prefix: int) -> torch.Tensor:
         return torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, n_prefix, self.N), dtype=torch.uint8,
@@ -164,6 +168,8 @@ class Qi21Runner:
     def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
         """The cached step over the 4-bit prefix. accumulate: add every layer's
         attention weights of this step to kv4_scores [L][items][H][rows]."""
+        if self.kv4 is None:
+            raise ValueError("cached_step_kv4 needs a quantise_prefix before it")
         if accumulate and self.kv4_scores is None:
             k = self.kv4
             self.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix, dtype=torch.float32,

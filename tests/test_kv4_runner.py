@@ -56,3 +56,36 @@ def test_workspace_holds_the_step_after_every_eviction(B, shape, batch, P, N, ke
         _evict(r, keep)
         assert r.kv4.n_prefix == keep
         assert r.kv4_ws.numel() >= B.qi21_kv4_step_workspace_bytes(r.cfg, batch, keep, N), keep
+
+
+def test_calls_without_a_4_bit_prefix_are_refused(B):
+    """The constructor's runner (its buffers are not needed here) has no 4-bit prefix."""
+    from prefix_kv_cached_b200 import runner
+    w = C.make_workload("small64")
+    r = runner.Qi21Runner(w, B.QI21_DTYPE_F32, device="cpu", host_weights=C.host_weights(w, "float32"))
+    x = torch.zeros(r.Bn, r.N, r.shape.latent_ch)
+    with pytest.raises(ValueError, match="quantise_prefix"):
+        r.cached_step_kv4(x, x)
+    with pytest.raises(ValueError):
+        r.evict_prefix(3)
+
+
+def test_a_refused_quantisation_or_eviction_keeps_the_cache_before_it(B, monkeypatch):
+    r = _runner(B, C.SMALL, 2, 198, 300)
+    r.kv4 = r.kv4_buf = r.kv4_scores = r.kv4_ws = None
+    with monkeypatch.context() as m:
+        m.setattr(B, "qi21_kv4_quantize", lambda *a: B.QI21_ERR_CACHE_STATE)
+        with pytest.raises(B.Qi21Error):
+            r.quantise_prefix()
+    assert r.kv4 is None and r.kv4_buf is None
+    r.quantise_prefix()
+    k = r.kv4
+    r.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix)
+    before = (r.kv4, r.kv4_buf, r.kv4_scores, r.kv4_ws)
+    with monkeypatch.context() as m:
+        m.setattr(B, "qi21_kv4_quantize", lambda *a: B.QI21_ERR_CACHE_STATE)      # a failed extract, say
+        m.setattr(B, "qi21_kv4_evict", lambda *a: B.QI21_ERR_SHAPE)               # more protected than kept
+        for call in (r.quantise_prefix, lambda: r.evict_prefix(5, 6)):
+            with pytest.raises(B.Qi21Error):
+                call()
+            assert all(a is b for a, b in zip(before, (r.kv4, r.kv4_buf, r.kv4_scores, r.kv4_ws)))
