@@ -78,16 +78,7 @@ class Qi21Runner:
                 raise ValueError(f"weight {name}: expected a contiguous {sdt} tensor on {self.device}")
             self.weights[name] = t
         self.wstruct = B.qi21_weights(*[self.weights[n].data_ptr() for n in WEIGHT_NAMES])
-        if shared_prefix:
-            kvb = B.qi21_kv_cache_bytes_shared(self.cfg, self.Bn, self.P, self.N)
-            self.cache_buf = torch.zeros(kvb, dtype=torch.uint8, device=self.device)
-            self.cache = B.qi21_kv_cache_init_shared(self.cache_buf, self.cfg, self.Bn, self.P, self.N)
-        else:
-            kvb = B.qi21_kv_cache_bytes(self.cfg, self.Bn, self.P, self.N)
-            self.cache_buf = torch.zeros(kvb, dtype=torch.uint8, device=self.device)
-            self.cache = B.qi21_kv_cache_init(self.cache_buf, self.cfg, self.Bn, self.P, self.N)
-        self.ws_bytes = B.qi21_workspace_bytes(self.cfg, self.Bn, self.P, self.N)
-        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._allocate()
         nch = 6 if sh.use_shift else 4
         self.mod_prefix = torch.zeros(nch * sh.d_model, dtype=torch.float32, device=self.device)
         self.mod_target = torch.zeros_like(self.mod_prefix)
@@ -99,14 +90,57 @@ class Qi21Runner:
         self.kv4_scores: Optional[torch.Tensor] = None
         self.kv4_ws: Optional[torch.Tensor] = None
 
+    def _allocate(self):
+        """The K/V cache, empty, and the workspace."""
+        if self.shared_prefix:
+            kvb = B.qi21_kv_cache_bytes_shared(self.cfg, self.Bn, self.P, self.N)
+            self.cache_buf = torch.zeros(kvb, dtype=torch.uint8, device=self.device)
+            self.cache = B.qi21_kv_cache_init_shared(self.cache_buf, self.cfg, self.Bn, self.P, self.N)
+        else:
+            kvb = B.qi21_kv_cache_bytes(self.cfg, self.Bn, self.P, self.N)
+            self.cache_buf = torch.zeros(kvb, dtype=torch.uint8, device=self.device)
+            self.cache = B.qi21_kv_cache_init(self.cache_buf, self.cfg, self.Bn, self.P, self.N)
+        self.ws_bytes = B.qi21_workspace_bytes(self.cfg, self.Bn, self.P, self.N)
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
     @property
     def stream(self) -> int:
         return torch.cuda.current_stream(self.device).cuda_stream
 
+    def _in_use(self, *buffers: Optional[torch.Tensor]):
+        """The current stream has work on these buffers. A later call, on whatever
+        stream, may drop them; the allocator must not give their memory to the stream
+        they were allocated on before this work is done."""
+        if self.device.type == "cuda":
+            s = torch.cuda.current_stream(self.device)
+            for t in buffers:
+                if t is not None:
+                    t.record_stream(s)
+
+    def _extracting(self):
+        """Before a call that needs the cache and the workspace, whatever the cache holds."""
+        if self.ws is None:
+            self._allocate()
+        self._in_use(self.cache_buf, self.ws)
+
+    def _extracted(self):
+        """Before a call that reads the extracted cache."""
+        if self.ws is None:
+            raise ValueError("the extracted cache was released; this needs a prefix_extract before it")
+        self._in_use(self.cache_buf, self.ws)
+
+    def _any_ws(self) -> torch.Tensor:
+        """The workspace, or once it is released that of the 4-bit steps (the calls of a
+        step use one after the other)."""
+        ws = self.kv4_ws if self.ws is None else self.ws
+        self._in_use(ws)
+        return ws
+
     # ------------------------------------------------------------------ calls
     def modulation(self, t: float, mod_row: torch.Tensor, scale_final: torch.Tensor):
-        B.check("qi21_modulation", B.qi21_modulation(self.cfg, self.wstruct, t, mod_row, scale_final, self.ws,
-                                                     self.ws_bytes, self.stream))
+        ws = self._any_ws()
+        B.check("qi21_modulation", B.qi21_modulation(self.cfg, self.wstruct, t, mod_row, scale_final, ws,
+                                                     ws.numel(), self.stream))
 
     def set_prefix_row(self):
         """Prefix modulation row at t = 0 (3B page: prefix tokens read t = 0)."""
@@ -115,22 +149,26 @@ class Qi21Runner:
     def set_target_row(self, sigma: float):
         """Target modulation row and final scale at noise level sigma (the library
         forms t = QI21_T_PER_SIGMA * sigma)."""
+        ws = self._any_ws()
         B.check("qi21_modulation_sigma", B.qi21_modulation_sigma(self.cfg, self.wstruct, float(sigma),
-                                                                 self.mod_target, self.scale_final, self.ws,
-                                                                 self.ws_bytes, self.stream))
+                                                                 self.mod_target, self.scale_final, ws,
+                                                                 ws.numel(), self.stream))
 
     def prefix_extract(self, prefix_hidden: torch.Tensor, mod_prefix: Optional[torch.Tensor] = None):
+        self._extracting()
         B.check("qi21_prefix_extract", B.qi21_prefix_extract(
             self.cfg, self.wstruct, self.cache, prefix_hidden, self.cos_sin_prefix, self.kv_limit_prefix,
             self.mod_prefix if mod_prefix is None else mod_prefix, self.ws, self.ws_bytes, self.stream))
 
     def cached_step(self, x: torch.Tensor, v_out: torch.Tensor):
+        self._extracted()
         B.check("qi21_cached_step", B.qi21_cached_step(
             self.cfg, self.wstruct, self.cache, x, self.cos_sin_target, self.mod_target, self.scale_final, v_out,
             self.ws, self.ws_bytes, self.stream))
 
     def full_recompute(self, prefix_hidden: torch.Tensor, x: torch.Tensor, v_out: torch.Tensor,
                        mod_prefix: Optional[torch.Tensor] = None):
+        self._extracting()
         B.check("qi21_full_recompute_step", B.qi21_full_recompute_step(
             self.cfg, self.wstruct, self.Bn, self.P, self.N, prefix_hidden, x, self.cos_sin_all, self.kv_limit_all,
             self.mod_prefix if mod_prefix is None else mod_prefix, self.mod_target, self.scale_final, v_out,
@@ -141,29 +179,26 @@ class Qi21Runner:
 
     # ------------------------------------------------------------------ 4-bit prefix cache
 
-    def quantise_prefix(self):
-        """Hold the extracted prefix in 4 bits from here on (for cached_step_kv4);
-        the cache buffer itself is kept for the next extract."""
+    def quantise_prefix(self, release: bool = False):
+        """Hold the extracted prefix in 4 bits from here on (for cached_step_kv4). The
+        extracted cache and its workspace are kept for the next extract, or, with
+        release, given back to the allocator: the 4-bit steps do without them, the next
+        prefix_extract allocates them again, and a graph of capture_image made before
+        must not be replayed any more."""
+        self._extracted()
         nb = 1 if self.shared_prefix else self.Bn
         buf = torch.empty(B.qi21_kv4_cache_bytes(self.cfg, nb, self.P), dtype=torch.uint8, device=self.device)
         cache4 = B.qi21_kv4_cache_init(buf, self.cfg, nb, self.P)
         ws = self._kv4_workspace(self.P)
         B.check("qi21_kv4_quantize", B.qi21_kv4_quantize(self.cfg, self.cache, cache4, self.stream))
         self.kv4, self.kv4_buf, self.kv4_scores, self.kv4_ws = cache4, buf, None, ws
+        if release:
+            self.cache.state, self.cache.base = B.QI21_CACHE_EMPTY, None
+            self.cache_buf = self.ws = None
 
     def _kv4_workspace(self, n_prefix: int) -> torch.Tensor:
         return torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, n_prefix, self.N), dtype=torch.uint8,
                            device=self.device)
-
-    def _kv4_in_use(self):
-        """The current stream has work on the 4-bit buffers. Later calls, on whatever
-        stream, drop them; the allocator must not give their memory to the stream they
-        were allocated on before this work is done."""
-        if self.device.type == "cuda":
-            s = torch.cuda.current_stream(self.device)
-            for t in (self.kv4_buf, self.kv4_ws, self.kv4_scores):
-                if t is not None:
-                    t.record_stream(s)
 
     def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
         """The cached step over the 4-bit prefix. accumulate: add every layer's
@@ -174,7 +209,7 @@ class Qi21Runner:
             k = self.kv4
             self.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix, dtype=torch.float32,
                                           device=self.device)
-        self._kv4_in_use()
+        self._in_use(self.kv4_buf, self.kv4_ws, self.kv4_scores)
         B.check("qi21_cached_step_kv4", B.qi21_cached_step_kv4(
             self.cfg, self.wstruct, self.kv4, self.Bn, self.N, x, self.cos_sin_target, self.mod_target,
             self.scale_final, v_out, self.kv4_scores if accumulate else None, self.kv4_ws, self.kv4_ws.numel(),
@@ -194,7 +229,7 @@ class Qi21Runner:
         need = B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, keep, self.N)
         ws = self.kv4_ws if self.kv4_ws.numel() >= need else self._kv4_workspace(keep)
         kept = torch.empty(k.n_layers, k.batch, k.n_heads, keep, dtype=torch.int32, device=self.device)
-        self._kv4_in_use()
+        self._in_use(self.kv4_buf, self.kv4_ws, self.kv4_scores)
         B.check("qi21_kv4_evict", B.qi21_kv4_evict(self.cfg, k, self.kv4_scores, keep, n_protected, small, kept,
                                                    self.stream))
         self.kv4, self.kv4_buf, self.kv4_scores = small, buf, None
@@ -202,13 +237,14 @@ class Qi21Runner:
         return kept
 
     def denoise_kv4(self, prefix_hidden: torch.Tensor, x0: torch.Tensor, sigmas=None, keep: Optional[int] = None,
-                    n_protected: int = 0):
+                    n_protected: int = 0, release: bool = False):
         """denoise() with the prefix held in 4 bits; keep: after the first step, go
-        on with the `keep` prefix rows of every head that it attended to most."""
+        on with the `keep` prefix rows of every head that it attended to most; release:
+        as in quantise_prefix."""
         sigmas = self.w.sigmas if sigmas is None else sigmas
         self.set_prefix_row()
         self.prefix_extract(prefix_hidden)
-        self.quantise_prefix()
+        self.quantise_prefix(release)
         x = x0.clone()
         v = torch.empty_like(x)
         for k in range(len(sigmas) - 1):
@@ -228,6 +264,7 @@ class Qi21Runner:
         place (x_0 in, final latent out). sigmas_dev: float64 device tensor."""
         assert sigmas_dev.dtype == torch.float64 and sigmas_dev.is_cuda and sigmas_dev.numel() >= 2
         v = torch.empty_like(x) if v is None else v
+        self._extracting()
         B.check("qi21_denoise_image", B.qi21_denoise_image(
             self.cfg, self.wstruct, self.cache, prefix_hidden, self.cos_sin_prefix, self.kv_limit_prefix,
             self.cos_sin_target, sigmas_dev, sigmas_dev.numel() - 1, B.QI21_T_PER_SIGMA, x, v, self.mod_prefix,
@@ -252,11 +289,13 @@ class Qi21Runner:
         return g
 
     def check_device(self):
-        B.check("qi21_check_device_error", B.qi21_check_device_error(self.ws, self.ws_bytes, self.stream))
+        ws = self._any_ws()
+        B.check("qi21_check_device_error", B.qi21_check_device_error(ws, ws.numel(), self.stream))
 
     def cache_kv(self):
         """Views of the cache as K, V [L][B][P+N][H][Dh] (for tests); with a shared
         prefix, [L][Pp + B*N][H][Dh] (prefix rows [0, P), request b at Pp + b*N)."""
+        self._extracted()
         sh = self.shape
         if self.shared_prefix:
             pp = -(-self.P // 128) * 128

@@ -106,3 +106,60 @@ def test_requantising_under_a_step_on_another_stream(B, mid):
     torch.cuda.synchronize()
     # bf16: the GEMMs add their last partial tiles in no fixed order
     assert (v - want).norm() < 1e-2 * want.norm()
+
+
+@pytest.fixture(scope="module")
+def small(B):
+    """Three requests of the small64 workload in float32, whose steps give the same bits every time."""
+    import dataclasses
+    from prefix_kv_cached_b200.runner import Qi21Runner
+    w = dataclasses.replace(C.make_workload("small64"), batch=3)
+    return Qi21Runner(w, B.QI21_DTYPE_F32, host_weights=C.host_weights(w, "float32"))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_release_frees_the_extracted_cache_and_its_workspace(B, small, shared):
+    """The steps, the eviction and the modulation rows go on without them, to the same
+    bits, and the next image extracts into new ones."""
+    from prefix_kv_cached_b200.runner import Qi21Runner
+    r = Qi21Runner(small.w, B.QI21_DTYPE_F32, share_weights_with=small, shared_prefix=shared)
+    pre, x0 = _inputs(r, 3)
+    pre = pre[:1].contiguous() if shared else pre
+    ordinary = r.denoise(pre, x0, r.w.sigmas[:3])
+    want = r.denoise_kv4(pre, x0, r.w.sigmas[:4], keep=30, n_protected=7)
+    held = r.cache_buf.numel() + r.ws.numel()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    got = r.denoise_kv4(pre, x0, r.w.sigmas[:4], keep=30, n_protected=7, release=True)
+    torch.cuda.synchronize()
+    assert before - torch.cuda.memory_allocated() >= held - 4 * got.numel() - 1024      # `got` is new
+    assert torch.equal(got, want)
+    with pytest.raises(ValueError, match="released"):
+        r.cached_step(x0, torch.empty_like(x0))
+    assert torch.equal(r.denoise_kv4(pre, x0, r.w.sigmas[:4], keep=30, n_protected=7, release=True), want)
+    assert torch.equal(r.denoise(pre, x0, r.w.sigmas[:3]), ordinary)                    # extracted anew
+    r.check_device()
+
+
+def test_release_under_a_step_on_another_stream(B, small):
+    """An ordinary step on another stream still reads the extracted cache when it is
+    released: its memory stays out of use until the step is done."""
+    from prefix_kv_cached_b200.runner import Qi21Runner
+    r = Qi21Runner(small.w, B.QI21_DTYPE_F32, share_weights_with=small)
+    pre, x0 = _inputs(r, 4)
+    want, v = torch.empty_like(x0), torch.empty_like(x0)
+    _quantised(r, pre)
+    r.cached_step(x0, want)
+    torch.cuda.synchronize()
+    old = [(t.data_ptr(), t.numel()) for t in (r.cache_buf, r.ws)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(WAIT)
+        r.cached_step(x0, v)
+    r.quantise_prefix(release=True)
+    taken = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for _, n in old]
+    assert not side.query()
+    for t in taken:
+        assert all(t.data_ptr() + t.numel() <= p or p + n <= t.data_ptr() for p, n in old)
+    torch.cuda.synchronize()
+    assert torch.equal(v, want)

@@ -32,7 +32,8 @@ def _runner(B, shape, batch, P, N, shared=False):
     from prefix_kv_cached_b200.runner import Qi21Runner, make_config
     r = object.__new__(Qi21Runner)
     r.device, r.cfg = torch.device("cpu"), make_config(shape, B.QI21_DTYPE_BF16)
-    r.Bn, r.P, r.N, r.shared_prefix, r.cache = batch, P, N, shared, None
+    r.Bn, r.P, r.N, r.shared_prefix = batch, P, N, shared
+    r._allocate()
     return r
 
 
@@ -89,3 +90,26 @@ def test_a_refused_quantisation_or_eviction_keeps_the_cache_before_it(B, monkeyp
             with pytest.raises(B.Qi21Error):
                 call()
             assert all(a is b for a, b in zip(before, (r.kv4, r.kv4_buf, r.kv4_scores, r.kv4_ws)))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_release_gives_the_extracted_cache_back(B, shared):
+    r = _runner(B, C.SMALL, 2, 198, 300, shared)
+    size = r.cache_buf.numel()
+    r.quantise_prefix()
+    assert r.cache_buf is not None and r.ws is not None              # kept unless asked
+    old = r.cache
+    old.state = B.QI21_CACHE_EXTRACTED
+    r.quantise_prefix(release=True)
+    assert r.cache_buf is None and r.ws is None
+    assert old.state == B.QI21_CACHE_EMPTY and not old.base          # no address of freed memory is left
+    x = torch.zeros(1)
+    for call in (lambda: r.cached_step(x, x), r.cache_kv, r.quantise_prefix):
+        with pytest.raises(ValueError, match="released"):
+            call()
+    _evict(r, 50)                                                    # the 4-bit cache goes on
+    assert r.kv4.n_prefix == 50
+    # the workspace of the modulation is part of every step's
+    assert r.kv4_ws.numel() >= B.qi21_workspace_bytes(r.cfg, 1, 0, 1)
+    r._extracting()                                                  # as every call does that fills the cache
+    assert r.cache_buf.numel() == size and r.ws.numel() == r.ws_bytes and r.cache.state == B.QI21_CACHE_EMPTY
