@@ -193,12 +193,23 @@ class Qi21Runner:
         B.check("qi21_kv4_quantize", B.qi21_kv4_quantize(self.cfg, self.cache, cache4, self.stream))
         self.kv4, self.kv4_buf, self.kv4_scores, self.kv4_ws = cache4, buf, None, ws
         if release:
+            self._carry_error(self.ws, ws)
             self.cache.state, self.cache.base = B.QI21_CACHE_EMPTY, None
             self.cache_buf = self.ws = None
 
     def _kv4_workspace(self, n_prefix: int) -> torch.Tensor:
-        return torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, n_prefix, self.N), dtype=torch.uint8,
-                           device=self.device)
+        """A workspace of the 4-bit steps, to take the place of the present one."""
+        ws = torch.zeros(B.qi21_kv4_step_workspace_bytes(self.cfg, self.Bn, n_prefix, self.N), dtype=torch.uint8,
+                         device=self.device)
+        self._carry_error(self.kv4_ws, ws)
+        return ws
+
+    def _carry_error(self, old: Optional[torch.Tensor], new: torch.Tensor):
+        """A workspace begins with the device error word that check_device reads; what a
+        kernel reported in one that is dropped goes into the next."""
+        if old is not None:
+            self._in_use(old)
+            new[:4].bitwise_or_(old[:4])
 
     def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
         """The cached step over the 4-bit prefix. accumulate: add every layer's
@@ -289,8 +300,10 @@ class Qi21Runner:
         return g
 
     def check_device(self):
-        ws = self._any_ws()
-        B.check("qi21_check_device_error", B.qi21_check_device_error(ws, ws.numel(), self.stream))
+        for ws in (self.ws, self.kv4_ws):
+            if ws is not None:
+                self._in_use(ws)
+                B.check("qi21_check_device_error", B.qi21_check_device_error(ws, ws.numel(), self.stream))
 
     def cache_kv(self):
         """Views of the cache as K, V [L][B][P+N][H][Dh] (for tests); with a shared

@@ -33,6 +33,7 @@ def _runner(B, shape, batch, P, N, shared=False):
     r = object.__new__(Qi21Runner)
     r.device, r.cfg = torch.device("cpu"), make_config(shape, B.QI21_DTYPE_BF16)
     r.Bn, r.P, r.N, r.shared_prefix = batch, P, N, shared
+    r.kv4 = r.kv4_buf = r.kv4_scores = r.kv4_ws = None
     r._allocate()
     return r
 
@@ -113,3 +114,30 @@ def test_release_gives_the_extracted_cache_back(B, shared):
     assert r.kv4_ws.numel() >= B.qi21_workspace_bytes(r.cfg, 1, 0, 1)
     r._extracting()                                                  # as every call does that fills the cache
     assert r.cache_buf.numel() == size and r.ws.numel() == r.ws_bytes and r.cache.state == B.QI21_CACHE_EMPTY
+
+
+def test_check_device_reads_what_the_4_bit_steps_reported(B, monkeypatch):
+    """The error word at a workspace's start: of both workspaces, and of those that a
+    quantisation, an eviction or a release has dropped."""
+    def check(ws, ws_bytes, stream=0):
+        found = ws[0].item()
+        ws[0] = 0
+        return B.QI21_ERR_DEVICE_TIMEOUT if found else B.QI21_OK
+
+    monkeypatch.setattr(B, "qi21_check_device_error", check)
+    r = _runner(B, C.MID, 8, 512, 256)
+    r.check_device()
+    r.quantise_prefix()
+    for drop in (lambda: None, r.quantise_prefix, lambda: _evict(r, 333), lambda: r.quantise_prefix(release=True)):
+        r.check_device()
+        r.kv4_ws[0] = 1
+        drop()
+        with pytest.raises(B.Qi21Error):
+            r.check_device()
+    r._extracting()
+    for drop in (lambda: None, lambda: r.quantise_prefix(release=True)):
+        r.check_device()
+        r.ws[0] = 1
+        drop()
+        with pytest.raises(B.Qi21Error):
+            r.check_device()
