@@ -213,10 +213,14 @@ class Qi21Runner:
 
     def cached_step_kv4(self, x: torch.Tensor, v_out: torch.Tensor, accumulate: bool = False):
         """The cached step over the 4-bit prefix. accumulate: add every layer's
-        attention weights of this step to kv4_scores [L][items][H][rows]."""
+        attention weights of this step to kv4_scores [L][items][H][rows]; the first such
+        step since quantise_prefix or evict_prefix makes them and cannot be captured."""
         if self.kv4 is None:
             raise ValueError("cached_step_kv4 needs a quantise_prefix before it")
         if accumulate and self.kv4_scores is None:
+            # captured, the zeros would be written again at every replay
+            if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                raise ValueError("capture a cached_step_kv4 with accumulate=True after one that was not captured")
             k = self.kv4
             self.kv4_scores = torch.zeros(k.n_layers, k.batch, k.n_heads, k.n_prefix, dtype=torch.float32,
                                           device=self.device)

@@ -163,3 +163,34 @@ def test_release_under_a_step_on_another_stream(B, small):
         assert all(t.data_ptr() + t.numel() <= p or p + n <= t.data_ptr() for p, n in old)
     torch.cuda.synchronize()
     assert torch.equal(v, want)
+
+
+def test_captured_steps_add_to_the_weights_of_the_one_before(B, small):
+    """A captured step adds its weights at every replay; the step that would make the
+    weights, and so clear them at every replay, is refused in a capture."""
+    from prefix_kv_cached_b200.runner import Qi21Runner
+    r = Qi21Runner(small.w, B.QI21_DTYPE_F32, share_weights_with=small)
+    pre, x0 = _inputs(r, 5)
+    v = torch.empty_like(x0)
+    _quantised(r, pre)
+    r.cached_step_kv4(x0, v)                               # sets kernel attributes
+    torch.cuda.synchronize()
+
+    def capture(g):
+        with torch.cuda.graph(g, capture_error_mode="thread_local"):
+            v.zero_()
+            r.cached_step_kv4(x0, v, accumulate=True)
+
+    with pytest.raises(ValueError, match="capture"):
+        capture(torch.cuda.CUDAGraph())
+    assert r.kv4_scores is None
+    r.cached_step_kv4(x0, v, accumulate=True)
+    one = r.kv4_scores.clone()
+    g = torch.cuda.CUDAGraph()
+    capture(g)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    # three float32 sums, each off by 2^-24 of it at most, against three times the first
+    assert ((r.kv4_scores - 3 * one).abs() <= 3 * 2.0 ** -23 * one).all() and (one > 0).any()
+    del g
