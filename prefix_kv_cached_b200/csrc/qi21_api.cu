@@ -296,16 +296,16 @@ static bool make_map4(CUtensorMap *m, const void *base, uint64_t inner, uint64_t
 
 template <int DH>
 static void launch_attn_tc(Launcher &L, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                           const AttnParams &p, int B) {
+                           const CUtensorMap &kt, const CUtensorMap &vt, const AttnParams &p, int B) {
     using Cf = AttnCfg<DH>;
     static DeviceFlags attr;
     smem_opt_in(k_attn_tc<DH>, (int)Cf::SMEM, attr);
     dim3 grid((p.Mq + Cf::BQ - 1) / Cf::BQ, p.H, B);
-    L.run("attn", [&] { launch_dep(k_attn_tc<DH>, grid, dim3(Cf::THREADS), Cf::SMEM, L.st, nullptr, q, k, v, p); });
+    L.run("attn", [&] { launch_dep(k_attn_tc<DH>, grid, dim3(Cf::THREADS), Cf::SMEM, L.st, nullptr, q, k, v, kt, vt, p); });
 }
 
 struct TcMaps {
-    CUtensorMap xn, o, hid, wq, wk, wv, wo, wg, wu, wd, q4, k4, v4, h32;
+    CUtensorMap xn, o, hid, wq, wk, wv, wo, wg, wu, wd, q4, k4, v4, kt4, vt4, h32;
 };
 
 static bool build_tc_maps(TcMaps &t, const qi21_config &c, const qi21_weights &w, const void *xn, const void *o,
@@ -420,13 +420,17 @@ static void run_stack(Launcher &L, const qi21_config &c, const qi21_weights &w, 
         const uint64_t nl = a.kv_layer_stride ? (uint64_t)c.n_layers : 1;
         const uint64_t lstride = a.kv_layer_stride ? (uint64_t)a.kv_layer_stride : (uint64_t)a.kv_bstride * a.B;
         bool ok = make_map4(&maps.q4, a.q, d, R, 1, 1, d, (uint64_t)R * d, (uint64_t)R * d);
-        if (a.shared) {   // one item of Pp + B*N rows per layer
-            const uint64_t rows_all = (uint64_t)a.shared_Pp + (uint64_t)a.B * a.N;
-            ok &= make_map4(&maps.k4, a.kv_k0, d, rows_all, 1, nl, d, rows_all * d, lstride);
-            ok &= make_map4(&maps.v4, a.kv_v0, d, rows_all, 1, nl, d, rows_all * d, lstride);
+        if (a.shared) {   // per layer the P rows of the prefix, and from row Pp on B items of N rows
+            const uint64_t pn = (uint64_t)a.shared_P, tgt = (uint64_t)a.shared_Pp * d, bs = a.kv_bstride;
+            ok &= make_map4(&maps.k4, a.kv_k0, d, pn, 1, nl, d, pn * d, lstride);
+            ok &= make_map4(&maps.v4, a.kv_v0, d, pn, 1, nl, d, pn * d, lstride);
+            ok &= make_map4(&maps.kt4, (const T *)a.kv_k0 + tgt, d, a.N, a.B, nl, d, bs, lstride);
+            ok &= make_map4(&maps.vt4, (const T *)a.kv_v0 + tgt, d, a.N, a.B, nl, d, bs, lstride);
         } else {
             ok &= make_map4(&maps.k4, a.kv_k0, d, a.kv_len, a.B, nl, d, a.kv_bstride, lstride);
             ok &= make_map4(&maps.v4, a.kv_v0, d, a.kv_len, a.B, nl, d, a.kv_bstride, lstride);
+            maps.kt4 = maps.k4;      // not used
+            maps.vt4 = maps.v4;
         }
         ok &= make_map_f32(&maps.h32, a.h, d, R);
         if (!ok) {
@@ -508,12 +512,11 @@ static void run_stack(Launcher &L, const qi21_config &c, const qi21_weights &w, 
                 ap.shared_tiles = a.shared_Pp / QI21_ATTN_KEY_TILE;
                 ap.prefix_len = a.shared_P;
                 ap.tgt_len = a.N;
-                ap.tgt_row0 = a.shared_Pp;
             }
             if (Dh == 128)
-                launch_attn_tc<128>(L, maps.q4, maps.k4, maps.v4, ap, a.B);
+                launch_attn_tc<128>(L, maps.q4, maps.k4, maps.v4, maps.kt4, maps.vt4, ap, a.B);
             else
-                launch_attn_tc<64>(L, maps.q4, maps.k4, maps.v4, ap, a.B);
+                launch_attn_tc<64>(L, maps.q4, maps.k4, maps.v4, maps.kt4, maps.vt4, ap, a.B);
         } else {
             const size_t smem = sizeof(float) * (3 * 32 * (Dh + 1) + 32 * 33);
             static DeviceFlags attr;

@@ -54,9 +54,11 @@ struct AttnParams {
     uint32_t *err;
     // Shared-prefix cache (one prefix for every item): key tiles [0, shared_tiles)
     // are prefix rows t*BK (keys >= prefix_len masked), the rest item b's target
-    // rows tgt_row0 + b*tgt_len + (t - shared_tiles)*BK (keys >= tgt_len masked).
+    // rows (t - shared_tiles)*BK (keys >= tgt_len masked), through tensor maps of
+    // their own. Either map ends with its rows, so that what lies behind them (other
+    // items' rows, rows [P, Pp)) is not loaded: a weight of 0 does not silence a NaN.
     // shared_tiles == 0: every item's keys are rows [0, kv_len) of its own block.
-    int shared_tiles, prefix_len, tgt_len, tgt_row0;
+    int shared_tiles, prefix_len, tgt_len;
 };
 
 // Further parameters of the two-buffer form (EXT): the prefix keys are rows of one
@@ -275,15 +277,11 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tmQ, const CUten
     const int T = EXT || p.shared_tiles > 0 ? p_tiles + (p.tgt_len + C::BK - 1) / C::BK
                                             : (kv_end + C::BK - 1) / C::BK;
     const int TA = (T + 1) >> 1, TB = T >> 1;     // tiles of half A and half B
-    // row and item coordinates of key tile t in the K/V tensor maps
-    auto tile_row = [&](int t) -> int {
-        if (EXT) return (t < p_tiles ? t : t - p_tiles) * C::BK;
-        if (p.shared_tiles == 0) return t * C::BK;
-        return t < p.shared_tiles ? t * C::BK : p.tgt_row0 + b * p.tgt_len + (t - p.shared_tiles) * C::BK;
-    };
+    // tensor map, row and item of key tile t
+    const bool two = EXT || p.shared_tiles > 0;
+    auto tail = [&](int t) -> bool { return two && t >= p_tiles; };      // by the second pair of maps
+    auto tile_row = [&](int t) -> int { return (tail(t) ? t - p_tiles : t) * C::BK; };
     const int kv_item = EXT ? (x.one_prefix ? 0 : b) : (p.shared_tiles > 0 ? 0 : b);
-    // the tensor map and item of tile t
-    auto tail = [&](int t) -> bool { return EXT && t >= p_tiles; };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producers
@@ -581,8 +579,9 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tmQ, const CUten
 template <int DH>
 __global__ void __launch_bounds__(320, 1)
     k_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnParams p) {
-    attn_tc_body<DH, false>(tmQ, tmK, tmV, tmK, tmV, p, AttnExt{});
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
+              const __grid_constant__ CUtensorMap tmVt, const __grid_constant__ AttnParams p) {
+    attn_tc_body<DH, false>(tmQ, tmK, tmV, tmKt, tmVt, p, AttnExt{});
 }
 
 // The two-buffer form: q [B][Mq][d]; tmK, tmV over the prefix buffer, tmKt, tmVt over

@@ -1,0 +1,85 @@
+"""Edges of the 4-bit prefix cache and of the caches it is read from and written to:
+memory that the caller never cleared, scores that are not finite, lengths."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from qi21_synth import configs as C
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from prefix_kv_cached_b200 import build
+    build.build()
+    from prefix_kv_cached_b200 import binding
+    return binding
+
+
+@pytest.fixture
+def mode(request, B):
+    """(dtype, torch dtype); switches the kernel family for the test."""
+    B.qi21_set_tensor_cores(0 if request.param == "bf16_cuda_cores" else 1)
+    yield (B.QI21_DTYPE_F32, torch.float32) if request.param == "f32" else (B.QI21_DTYPE_BF16, torch.bfloat16)
+    B.qi21_set_tensor_cores(1)
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _rel(a, b):
+    return float((a.double() - b.double()).norm() / b.double().norm())
+
+
+# ------------------------------------------------------------------ memory that nobody cleared
+
+@pytest.mark.parametrize("mode", ["f32", "bf16", "bf16_cuda_cores"], indirect=True)
+@pytest.mark.parametrize("name", ["small64", "small"])
+def test_shared_prefix_rows_behind_the_prefix_are_never_read(B, mode, name):
+    """A shared-prefix cache in memory full of NaNs, filled by an extract and by the way
+    back from 4 bits: rows [P, Pp) keep their NaNs, and the step gives what it gives in
+    cleared memory (P 130 or 198: the last key tile of the prefix ends behind them)."""
+    dtype, tdt = mode
+    from prefix_kv_cached_b200.runner import Qi21Runner
+    w = dataclasses.replace(C.make_workload(name), batch=2)
+    r = Qi21Runner(w, dtype, host_weights=C.host_weights(w, "float32" if tdt == torch.float32 else "bfloat16"),
+                   shared_prefix=True)
+    assert r.P % 128
+    pre = torch.randn(1, r.P, r.shape.d_model, device="cuda")
+    x0 = torch.randn(2, r.N, r.shape.latent_ch, device="cuda")
+    v, want = torch.empty_like(x0), torch.empty_like(x0)
+    r.set_prefix_row()
+    r.set_target_row(w.sigmas[0])
+
+    def pads():
+        return [t[:, r.P:-(-r.P // 128) * 128] for t in r.cache_kv()]
+
+    def steps(fill):
+        r.cache_buf.fill_(fill)
+        r.prefix_extract(pre)
+        r.cached_step(x0, v)
+        a = v.clone()
+        r.quantise_prefix()
+        r.cache_buf.fill_(fill)
+        B.check("dequantize", B.qi21_kv4_dequantize(r.cfg, r.kv4, r.cache, r.stream))
+        r.cached_step(x0, v)
+        return a, v.clone()
+
+    want = steps(0)
+    got = steps(0xFF)
+    assert all(t.isnan().all() for t in pads())
+    for a, b in zip(got, want):
+        assert a.isfinite().all()
+        # float32 steps give the same bits; bf16 ones agree to the order of the GEMMs' last sums
+        assert torch.equal(a, b) if tdt == torch.float32 else _rel(a, b) < 1e-2
+    # a request that is not finite leaves the others as they are
+    x0[1] = float("nan")
+    r.cached_step(x0, v)
+    assert v[1].isnan().all() and (torch.equal(v[0], want[1][0]) if tdt == torch.float32 else
+                                   _rel(v[0], want[1][0]) < 1e-2)
