@@ -444,7 +444,9 @@ qi21_status qi21_kv4_quantize(const qi21_config *cfg, const qi21_kv_cache *src, 
 
 /* The way back: the values of src, exactly, into the prefix rows of dst in the
  * config dtype (either layout; sizes as above). Rows behind an item's prefix_len
- * are left as they are. On success dst->state = QI21_CACHE_EXTRACTED. */
+ * are left as they are. On success dst->state = QI21_CACHE_EXTRACTED; where src has
+ * lengths it stays QI21_CACHE_EMPTY, since qi21_cached_step attends to all n_prefix
+ * rows of every item: a caller that has filled the others sets it. */
 qi21_status qi21_kv4_dequantize(const qi21_config *cfg, const qi21_kv4_cache *src, qi21_kv_cache *dst,
                                 void *stream);
 

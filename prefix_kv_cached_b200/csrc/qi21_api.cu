@@ -994,7 +994,8 @@ extern "C" qi21_status qi21_kv4_dequantize(const qi21_config *c, const qi21_kv4_
     if (c->dtype == QI21_DTYPE_BF16) launch_kv4_dequantize<bf16>(L, *c, *src, *dst);
     else launch_kv4_dequantize<float>(L, *c, *src, *dst);
     s = finish(L);
-    if (s == QI21_OK) dst->state = QI21_CACHE_EXTRACTED;
+    // rows behind a length are not written, and the cached step reads all n_prefix
+    if (s == QI21_OK && !src->prefix_len) dst->state = QI21_CACHE_EXTRACTED;
     return s;
 }
 

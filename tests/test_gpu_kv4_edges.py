@@ -83,3 +83,36 @@ def test_shared_prefix_rows_behind_the_prefix_are_never_read(B, mode, name):
     r.cached_step(x0, v)
     assert v[1].isnan().all() and (torch.equal(v[0], want[1][0]) if tdt == torch.float32 else
                                    _rel(v[0], want[1][0]) < 1e-2)
+
+
+# ------------------------------------------------------------------ lengths
+
+def _cfg(B, dtype, H, Dh, L=1):
+    return B.qi21_config(H * Dh, H, Dh, L, 2 * H * Dh, 64, 256, dtype, 0, 1e-6, 1e-6)
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def test_the_way_back_of_lengths_is_no_extracted_cache(B):
+    """The ordinary step attends to all n_prefix rows of every item; a cache in which
+    the rows behind the lengths were never written is refused until the caller says
+    that it is whole."""
+    cfg = _cfg(B, B.QI21_DTYPE_BF16, 4, 64)
+    src = torch.randn(1, 2, 2, 30 + 1, 256, device="cuda").bfloat16()
+    cache = B.qi21_kv_cache_init(src, cfg, 2, 30, 1)
+    cache.state = B.QI21_CACHE_EXTRACTED
+    back = torch.zeros_like(src)
+    for lens, state in ((None, B.QI21_CACHE_EXTRACTED), ([30, 11, 0, 0], B.QI21_CACHE_EMPTY)):
+        lt = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+        buf = torch.zeros(B.qi21_kv4_cache_bytes(cfg, 2, 30), dtype=torch.uint8, device="cuda")
+        k4 = B.qi21_kv4_cache_init(buf, cfg, 2, 30, lt)
+        assert B.qi21_kv4_quantize(cfg, cache, k4, _stream()) == B.QI21_OK
+        cb = B.qi21_kv_cache_init(back, cfg, 2, 30, 1)
+        assert B.qi21_kv4_dequantize(cfg, k4, cb, _stream()) == B.QI21_OK
+        assert cb.state == state
+        again = B.qi21_kv4_cache_init(torch.zeros_like(buf), cfg, 2, 30, lt)
+        if lens is not None:
+            assert B.qi21_kv4_quantize(cfg, cb, again, _stream()) == B.QI21_ERR_CACHE_STATE
+    torch.cuda.synchronize()
