@@ -490,7 +490,8 @@ qi21_status qi21_kv4_scores(const qi21_config *cfg, const qi21_kv4_cache *cache,
  *   kept [L][batch][H][keep] int32: the rows kept, ascending
  * An item with fewer than `keep` rows keeps all it has: kept is -1 behind them and
  * those rows of dst are left as they are. min(keep, length) is written to
- * dst->prefix_len where that is not NULL; it must be given where src has lengths.
+ * dst->prefix_len where that is not NULL; it must be given where src has lengths, and
+ * may not overlap them.
  * On success dst->state = QI21_CACHE_EXTRACTED. */
 qi21_status qi21_kv4_evict(const qi21_config *cfg, const qi21_kv4_cache *src, const float *scores,
                            int32_t keep, int32_t n_protected, qi21_kv4_cache *dst, int32_t *kept,

@@ -1056,7 +1056,10 @@ extern "C" qi21_status qi21_kv4_evict(const qi21_config *c, const qi21_kv4_cache
     const char *a = (const char *)src->base, *b = (const char *)dst->base;
     const size_t an = qi21_kv4_cache_bytes(c, src->batch, src->n_prefix), bn = qi21_kv4_cache_bytes(c, dst->batch, keep);
     if (a < b + bn && b < a + an) return QI21_ERR_INVALID_ARG;       // the gather is not in place
-    if (src->prefix_len && src->prefix_len == dst->prefix_len) return QI21_ERR_INVALID_ARG;
+    // one block writes a length that blocks of other heads still read
+    if (src->prefix_len && dst->prefix_len < src->prefix_len + src->batch &&
+        src->prefix_len < dst->prefix_len + dst->batch)
+        return QI21_ERR_INVALID_ARG;
     dst->state = QI21_CACHE_EMPTY;
     Launcher L((cudaStream_t)stream);
     launch_kv4_evict(L, *c, *src, scores, keep, n_protected, *dst, kept);
