@@ -437,13 +437,14 @@ qi21_status qi21_denoise_image(const qi21_config *cfg, const qi21_weights *w, qi
 /* Quantise the prefix rows of every layer of an extracted cache into dst (same
  * layers, heads and n_prefix; dst->batch = src->batch, or 1 for a shared-prefix
  * cache). Rows behind an item's prefix_len are neither read nor written. The
- * target rows of src stay out. src may be freed once the work is done.
+ * target rows of src stay out. src may be freed once the work is done; the buffers may
+ * not overlap.
  * On success dst->state = QI21_CACHE_EXTRACTED. */
 qi21_status qi21_kv4_quantize(const qi21_config *cfg, const qi21_kv_cache *src, qi21_kv4_cache *dst,
                               void *stream);
 
 /* The way back: the values of src, exactly, into the prefix rows of dst in the
- * config dtype (either layout; sizes as above). Rows behind an item's prefix_len
+ * config dtype (either layout; sizes and buffers as above). Rows behind an item's prefix_len
  * are left as they are. On success dst->state = QI21_CACHE_EXTRACTED; where src has
  * lengths it stays QI21_CACHE_EMPTY, since qi21_cached_step attends to all n_prefix
  * rows of every item: a caller that has filled the others sets it. */

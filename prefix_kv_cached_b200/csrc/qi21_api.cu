@@ -962,6 +962,10 @@ extern "C" qi21_status qi21_cached_step_kv4(const qi21_config *c, const qi21_wei
     return finish(L);
 }
 
+static bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+    return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+
 static qi21_status check_kv4_pair(const qi21_config *c, const qi21_kv_cache *a, const qi21_kv4_cache *k) {
     qi21_status s = check_shapes(c);
     if (s) return s;
@@ -970,11 +974,19 @@ static qi21_status check_kv4_pair(const qi21_config *c, const qi21_kv_cache *a, 
     return kv4_matches(c, a, k) ? QI21_OK : QI21_ERR_CACHE_STATE;
 }
 
+// Neither way works in place.
+static bool kv4_pair_overlaps(const qi21_config *c, const qi21_kv_cache *a, const qi21_kv4_cache *k) {
+    const size_t an = a->shared_prefix ? qi21_kv_cache_bytes_shared(c, a->batch, a->n_prefix, a->n_target)
+                                       : qi21_kv_cache_bytes(c, a->batch, a->n_prefix, a->n_target);
+    return overlap(a->base, an, k->base, qi21_kv4_cache_bytes(c, k->batch, k->n_prefix));
+}
+
 extern "C" qi21_status qi21_kv4_quantize(const qi21_config *c, const qi21_kv_cache *src, qi21_kv4_cache *dst,
                                          void *stream) {
     qi21_status s = check_kv4_pair(c, src, dst);
     if (s) return s;
     if (src->state != QI21_CACHE_EXTRACTED) return QI21_ERR_CACHE_STATE;
+    if (kv4_pair_overlaps(c, src, dst)) return QI21_ERR_INVALID_ARG;
     dst->state = QI21_CACHE_EMPTY;
     Launcher L((cudaStream_t)stream);
     if (c->dtype == QI21_DTYPE_BF16) launch_kv4_quantize<bf16>(L, *c, *src, *dst);
@@ -989,6 +1001,7 @@ extern "C" qi21_status qi21_kv4_dequantize(const qi21_config *c, const qi21_kv4_
     qi21_status s = check_kv4_pair(c, dst, src);
     if (s) return s;
     if (src->state != QI21_CACHE_EXTRACTED) return QI21_ERR_CACHE_STATE;
+    if (kv4_pair_overlaps(c, dst, src)) return QI21_ERR_INVALID_ARG;
     dst->state = QI21_CACHE_EMPTY;
     Launcher L((cudaStream_t)stream);
     if (c->dtype == QI21_DTYPE_BF16) launch_kv4_dequantize<bf16>(L, *c, *src, *dst);
@@ -1053,12 +1066,11 @@ extern "C" qi21_status qi21_kv4_evict(const qi21_config *c, const qi21_kv4_cache
     if (keep < 1 || keep > src->n_prefix || n_protected < 0 || n_protected > keep) return QI21_ERR_SHAPE;
     if (src->state != QI21_CACHE_EXTRACTED || dst->batch != src->batch || dst->n_prefix != keep)
         return QI21_ERR_CACHE_STATE;
-    const char *a = (const char *)src->base, *b = (const char *)dst->base;
-    const size_t an = qi21_kv4_cache_bytes(c, src->batch, src->n_prefix), bn = qi21_kv4_cache_bytes(c, dst->batch, keep);
-    if (a < b + bn && b < a + an) return QI21_ERR_INVALID_ARG;       // the gather is not in place
+    if (overlap(src->base, qi21_kv4_cache_bytes(c, src->batch, src->n_prefix), dst->base,
+                qi21_kv4_cache_bytes(c, dst->batch, keep)))
+        return QI21_ERR_INVALID_ARG;                                 // the gather is not in place
     // one block writes a length that blocks of other heads still read
-    if (src->prefix_len && dst->prefix_len < src->prefix_len + src->batch &&
-        src->prefix_len < dst->prefix_len + dst->batch)
+    if (src->prefix_len && overlap(src->prefix_len, 4 * (size_t)src->batch, dst->prefix_len, 4 * (size_t)dst->batch))
         return QI21_ERR_INVALID_ARG;
     dst->state = QI21_CACHE_EMPTY;
     Launcher L((cudaStream_t)stream);

@@ -29,3 +29,21 @@ def test_evict_lengths_that_overlap(B, src_len, dst_len):
     dst = B.qi21_kv4_cache_init(far, cfg, 9, 50, FAKE + dst_len)
     src.state = B.QI21_CACHE_EXTRACTED
     assert B.qi21_kv4_evict(cfg, src, FAKE, 50, 0, dst, FAKE) == B.QI21_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_quantise_and_the_way_back_in_place(B, shared):
+    """A 4-bit cache inside the cache it is made from, at its start, or across one end."""
+    cfg = _cfg(B)
+    base = FAKE + (1 << 30)
+    init, size = ((B.qi21_kv_cache_init_shared, B.qi21_kv_cache_bytes_shared) if shared else
+                  (B.qi21_kv_cache_init, B.qi21_kv_cache_bytes))
+    src = init(base, cfg, 2, 200, 300)
+    n, n4 = size(cfg, 2, 200, 300), B.qi21_kv4_cache_bytes(cfg, 1 if shared else 2, 200)
+    assert n > n4
+    for at in (base, base + 16, base + n - 16, base - n4 + 16):
+        k4 = B.qi21_kv4_cache_init(at, cfg, 1 if shared else 2, 200)
+        src.state = k4.state = B.QI21_CACHE_EXTRACTED
+        assert B.qi21_kv4_quantize(cfg, src, k4) == B.QI21_ERR_INVALID_ARG
+        assert B.qi21_kv4_dequantize(cfg, k4, src) == B.QI21_ERR_INVALID_ARG
+        assert src.state == k4.state == B.QI21_CACHE_EXTRACTED          # nothing has happened
