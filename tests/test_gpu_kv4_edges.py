@@ -116,3 +116,48 @@ def test_the_way_back_of_lengths_is_no_extracted_cache(B):
         if lens is not None:
             assert B.qi21_kv4_quantize(cfg, cb, again, _stream()) == B.QI21_ERR_CACHE_STATE
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ scores that are not finite
+
+@pytest.mark.parametrize("mode", ["f32", "bf16", "bf16_cuda_cores"], indirect=True)
+@pytest.mark.parametrize("H,Dh,N,P,T", [(2, 128, 1, 300, 140), (4, 64, 12, 300, 140), (2, 128, 60, 300, 140),
+                                        (4, 64, 200, 300, 140), (32, 128, 1025, 300, 140), (16, 64, 1200, 130, 129)])
+def test_an_infinite_score_makes_its_rows_nan(B, mode, H, Dh, N, P, T):
+    """One tail key after the other with an infinity in a head's last dim. A row whose
+    score there is +inf has the weight inf / inf: NaN, in the result and the log-sum-exp,
+    wherever the key lies in its tile; one whose score is -inf stays finite."""
+    dtype, tdt = mode
+    cfg = _cfg(B, dtype, H, Dh)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    src = torch.randn(1, 2, 1, P + 1, H * Dh, device="cuda", generator=gen).to(tdt)
+    cache = B.qi21_kv_cache_init(src, cfg, 1, P, 1)
+    cache.state = B.QI21_CACHE_EXTRACTED
+    buf = torch.zeros(B.qi21_kv4_cache_bytes(cfg, 1, P), dtype=torch.uint8, device="cuda")
+    k4 = B.qi21_kv4_cache_init(buf, cfg, 1, P)
+    B.check("quantize", B.qi21_kv4_quantize(cfg, cache, k4, _stream()))
+    q, kt, vt = (torch.randn(1, n, H * Dh, device="cuda", generator=gen).to(tdt) for n in (N, T, T))
+    q = torch.where(q == 0, torch.ones_like(q), q)                     # 0 * inf would be another NaN
+    n = B.qi21_kv4_workspace_bytes(cfg, 1, N, P, T)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(H, 1, N, device="cuda")
+
+    def run():
+        B.check("a", B.qi21_kv4_attention(cfg, k4, 0, q, 1, N, kt, vt, T, out, lse, ws, n, _stream()))
+        return out.view(N, H, Dh), lse[:, 0].T
+
+    for key in (0, 5, 13, 14, 15, 31, 47, 64, 111, 126, 127, T - 1):
+        h = key % H
+        row = kt[0, key, h * Dh:(h + 1) * Dh].clone()
+        kt[0, key, h * Dh:(h + 1) * Dh - 1] = 0                        # the score is q's last dim times it
+        kt[0, key, h * Dh + Dh - 1] = float("inf")
+        up = q[0, :, h * Dh + Dh - 1] > 0
+        o, l = run()
+        want = torch.zeros(N, H, dtype=torch.bool, device="cuda")
+        want[up, h] = True
+        assert torch.equal(o.isnan().all(-1), want) and torch.equal(o.isnan().any(-1), want), key
+        assert torch.equal(l.isnan(), want), key
+        assert not o.isinf().any() and not l.isinf().any()
+        kt[0, key, h * Dh:(h + 1) * Dh] = row
+    o, l = run()
+    assert o.isfinite().all() and l.isfinite().all()
