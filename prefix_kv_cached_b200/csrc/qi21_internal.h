@@ -125,10 +125,13 @@ constexpr int KV4_CUT_STEPS = 4;
 
 // The prefix is expanded once, instead of for every 256 rows, from KV4_EXPAND_ROWS
 // query rows on, where the 128-row query tiles fill the SMs, the prefix is no less than
-// the tail, and its bf16 copy stays in L2 (else from twice the rows on). us, expanded /
-// not, 32 heads of 128, as many tail keys as rows: P 4608: 4096 rows 459 / 530, 2048
-// rows 200 / 232, 1024 rows 97 / 120, 512 rows 69 / 69; P 33792 (553 MB): 2048 rows 1161
-// / 1166, 1024 rows 628 / 559. 8 x 16 heads of 64, P 512: 2048 rows 310 / 286.
+// the tail, and its bf16 copy stays in L2; where it does not, above twice the rows, since
+// up to there the copy's memory buys nothing. us, expanded / not, 32 heads of 128, as
+// many tail keys as rows: P 4608: 4096 rows 459 / 530, 2048 rows 200 / 232, 1024 rows 97
+// / 120, 512 rows 69 / 69; P 33792 (a copy of 553 MB): 1024 rows 628 / 559, 2048 rows
+// 1069 / 1070, 2176 rows 1093 / 1170, 2432 rows 1486 / 1469, 2944 rows 1497 / 1855, 4096
+// rows 2145 / 2490; P 12000 (197 MB): 2048 rows 508 / 523, 2304 rows 517 / 572. 8 x 16
+// heads of 64, P 512: 2048 rows 310 / 286; P 8000 (262 MB): 2304 rows 1190 / 1247.
 constexpr int KV4_EXPAND_ROWS = 1024;
 constexpr int64_t KV4_EXPAND_L2 = 96 << 20;     // of 126 MB
 // Up to this many query rows the few-rows kernels. us, 32 heads of 128, P 33792:
@@ -175,7 +178,7 @@ inline Kv4Plan kv4_plan(const qi21_config &c, int64_t items, int64_t B, int64_t 
         p.w.slot_rows = (int)(qt == 1 ? n_q : ur);
         if (units > INT32_MAX) p.ok = false;
         const int64_t copy = 4 * items * tp * 128 * c.d_model;
-        p.expanded = n_q >= (copy <= KV4_EXPAND_L2 ? 1 : 2) * KV4_EXPAND_ROWS && P >= n_tail &&
+        p.expanded = (copy <= KV4_EXPAND_L2 ? n_q >= KV4_EXPAND_ROWS : n_q > 2 * KV4_EXPAND_ROWS) && P >= n_tail &&
                      B * H * ((n_q + 127) / 128) >= KV4_SMS;
         if (p.expanded && (B > 65535 || (n_q + 127) / 128 > INT32_MAX)) p.ok = false;
         rows = p.w.whole || p.expanded ? 0 : (size_t)2 * p.w.grid * p.w.slot_rows;

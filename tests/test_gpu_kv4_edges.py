@@ -161,3 +161,39 @@ def test_an_infinite_score_makes_its_rows_nan(B, mode, H, Dh, N, P, T):
         kt[0, key, h * Dh:(h + 1) * Dh] = row
     o, l = run()
     assert o.isfinite().all() and l.isfinite().all()
+
+
+def test_long_prefix_around_the_rows_from_which_it_is_copied(B):
+    """2048 and 2049 rows over a prefix whose copy does not stay in L2 (16 heads of 64,
+    P 25000) take different kernels, fused and over the copy; each within the rounding
+    of weights and result of 64 bits on sampled rows."""
+    H, Dh, P, T = 16, 64, 25000, 40
+    cfg = _cfg(B, B.QI21_DTYPE_BF16, H, Dh)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    src = torch.randn(1, 2, 1, P + 1, H * Dh, device="cuda", generator=gen).bfloat16()
+    cache = B.qi21_kv_cache_init(src, cfg, 1, P, 1)
+    cache.state = B.QI21_CACHE_EXTRACTED
+    buf = torch.zeros(B.qi21_kv4_cache_bytes(cfg, 1, P), dtype=torch.uint8, device="cuda")
+    k4 = B.qi21_kv4_cache_init(buf, cfg, 1, P)
+    B.check("quantize", B.qi21_kv4_quantize(cfg, cache, k4, _stream()))
+    B.check("back", B.qi21_kv4_dequantize(cfg, k4, cache, _stream()))
+    k, v = (src[0, i, 0, :P].double().view(P, H, Dh) for i in range(2))
+    kt, vt = (torch.randn(1, T, H * Dh, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    k, v = (torch.cat((a, t[0].double().view(T, H, Dh))) for a, t in ((k, kt), (v, vt)))
+    sizes = []
+    for N in (2048, 2049):
+        q = torch.randn(1, N, H * Dh, device="cuda", generator=gen).bfloat16()
+        sizes.append(B.qi21_kv4_workspace_bytes(cfg, 1, N, P, T))
+        ws = torch.zeros(sizes[-1], dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(q), torch.empty(H, 1, N, device="cuda")
+        B.check("a", B.qi21_kv4_attention(cfg, k4, 0, q, 1, N, kt, vt, T, out, lse, ws, sizes[-1], _stream()))
+        B.check("device", B.qi21_check_device_error(ws, sizes[-1], _stream()))
+        for i in (0, 127, 128, 1000, N - 1):
+            x = torch.einsum("hd,jhd->hj", q[0, i].double().view(H, Dh), k) / Dh ** 0.5
+            w = x.softmax(-1)
+            o, mag = torch.einsum("hj,jhd->hd", w, v), torch.einsum("hj,jhd->hd", w, v.abs())
+            got = out[0, i].double().view(H, Dh)
+            # weights and result in bf16, half a step of 2^-8 each; fp32 sums 2e-5
+            assert ((got - o).abs() <= 2.0 ** -8 * (mag + o.abs()) + 2e-5 * mag).all()
+            assert (lse[:, 0, i] - x.logsumexp(-1)).abs().max() <= 2e-5
+    assert sizes[1] - sizes[0] > 2 * P * H * Dh            # the copy, less the partial results

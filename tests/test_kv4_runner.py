@@ -141,3 +141,11 @@ def test_check_device_reads_what_the_4_bit_steps_reported(B, monkeypatch):
         drop()
         with pytest.raises(B.Qi21Error):
             r.check_device()
+
+
+def test_a_copy_of_the_prefix_is_paid_for_where_it_is_faster(B):
+    """The attention over a long prefix in the 4-bit cache's own workspace up to 2048
+    rows; the bf16 copy of the layer (twice 33792 rows of 4096) only above."""
+    cfg, copy = _runner(B, H32, 1, 1, 1).cfg, 2 * 33792 * 4096 * 2
+    assert B.qi21_kv4_workspace_bytes(cfg, 1, 2048, 33792, 2048) < copy // 10
+    assert copy < B.qi21_kv4_workspace_bytes(cfg, 1, 4096, 33792, 4096) < copy + (1 << 20)
