@@ -53,7 +53,6 @@ struct Kv4Lop {
 };
 constexpr Kv4Lop kKv4Lop{0x00780078u, 0x41804180u};
 
-// (nibble - 8) s of the 8 nibbles of a code word as bf16 pairs in the order of dims.
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -73,6 +72,8 @@ __device__ __forceinline__ uint32_t kv4_nibbles(uint32_t w, const Kv4Lop &k) {
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(k.mask), "r"(k.one));   // (w & mask) | one
     return d;
 }
+// (nibble - 8) s of the 8 nibbles of a code word as bf16 pairs: in the order in which it
+// unfolds (nibbles i and i + 4), and in the order of dims.
 __device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t s2, uint32_t off2, const Kv4Lop &k, uint32_t (&p)[4]) {
     p[0] = fma_bf16x2(kv4_nibbles(w << 3, k), s2, off2);
     p[1] = fma_bf16x2(kv4_nibbles(w >> 1, k), s2, off2);

@@ -1,5 +1,7 @@
 // Launches of the 4-bit prefix cache's operators and their argument checks
-// (included by qi21_api.cu; the kernels are in qi21_kv4.cuh).
+// (included by qi21_api.cu; the kernels are in qi21_kv4.cuh, qi21_kv4_attn_tc.cuh,
+// qi21_kv4_rows.cuh, qi21_kv4_scores_tc.cuh and, over the expanded prefix,
+// qi21_attn_tc.cuh).
 #pragma once
 #include "qi21_kv4.cuh"
 #include "qi21_kv4_attn_tc.cuh"

@@ -3,7 +3,8 @@
 // The codes become bf16 in shared memory, next to the MMAs that read them, so
 // only 4.5 bits an element cross HBM and L2. The values of the format are exact
 // in bf16: S = Q K^T and O = P V are the products a bf16 cache holding the same
-// values would give.
+// values would give. The weights P are rounded to bf16 (2^-8 of each at most), because
+// both operands of a product have one type; sums, maxima and outputs are fp32.
 //
 // Work is cut into steps of one 128-key tile of one unit (item, head, query
 // tile); the steps of all units, laid end to end, are shared out evenly over one

@@ -21,10 +21,15 @@
 // cluster (else by k_kv4_combine), in a fixed order.
 // (tcgen05 would want the expanded cache in shared memory: 2 bytes an element
 // written and read again, which alone is as long as the read of 4.5 bits from HBM.)
-// Bound by the expansion's instructions (337 for 16 keys of K and V at head_dim 128,
-// 159 of them on the ALU pipe at half rate): 50 us for one row over P 33792, 32 heads of
-// 128 (3.1 TB/s), of which the pass over the key splits' results takes some 8; the loads
-// alone run 29 us, HBM's own time is 24.
+// The weights are rounded to bf16 for the product with V (2^-8 of each at most): its
+// operands have one type, and V's values are exact in bf16. Sums, maxima and outputs are
+// fp32.
+// Bound by latency: a scheduler has three warps, and each is a single chain of expansion,
+// product, maximum over shuffles, exponentials, transpose, expansion and product. 16 keys
+// of K and V at head_dim 128 take 575 cycles, of which the 159 instructions of the
+// expansion on the ALU pipe at half rate fill 318 (ALU 49 %, issue slots 52 %): 50 us for
+// one row over P 33792, 32 heads of 128 (3.1 TB/s), of which the pass over the key
+// splits' results takes some 8; the loads alone run 29 us, HBM's own time is 24.
 #pragma once
 #include "qi21_kv4_attn_tc.cuh"
 
