@@ -52,21 +52,30 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // Bounded wait: returns false (after raising the device error word and the
 // CTA's abort flag) if the phase does not complete within ~2 s, or if another
 // role of the CTA has already aborted. Never traps.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// A wait that fails returns 1 ms after it gave up: the CTA's copies in flight (loads that
+// nobody waits for any more) take a thousandth of that, and must not land in shared memory
+// that the CTA has left or writes over.
+constexpr uint64_t kWaitLimitNs = 2000000000ull, kSettleNs = 1000000ull;
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
                                           uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
+    uint64_t t0 = globaltimer();
+    bool failed = false;
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > limit_ns) {
-            *abort_flag = 1;
-            raise_device_error(err, DEV_ERR_TIMEOUT);
-            return false;
+            if (mbar_try_wait(bar, parity) && !failed) return true;
+        const uint64_t waited = globaltimer() - t0;
+        if (failed) {
+            if (waited > kSettleNs) return false;
+        } else if (*abort_flag || waited > limit_ns) {
+            if (!*abort_flag) {
+                *abort_flag = 1;
+                raise_device_error(err, DEV_ERR_TIMEOUT);
+            }
+            failed = true;
+            t0 = globaltimer();
         }
     }
 }

@@ -197,3 +197,20 @@ def test_long_prefix_around_the_rows_from_which_it_is_copied(B):
             assert ((got - o).abs() <= 2.0 ** -8 * (mag + o.abs()) + 2e-5 * mag).all()
             assert (lse[:, 0, i] - x.logsumexp(-1)).abs().max() <= 2e-5
     assert sizes[1] - sizes[0] > 2 * P * H * Dh            # the copy, less the partial results
+
+
+# ------------------------------------------------------------------ after a wait that failed
+
+def test_a_failed_wait_leaves_its_copies_time_to_land(B):
+    """The bounded wait of the self test (2 ms) gives up and returns a millisecond later,
+    in which copies into the block's shared memory can land, and no later."""
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    B.check("warm", B.qi21_selftest_wait_timeout(ws, ws.numel(), 1000, _stream()))
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    a.record()
+    B.check("selftest", B.qi21_selftest_wait_timeout(ws, ws.numel(), 2_000_000, _stream()))
+    b.record()
+    torch.cuda.synchronize()
+    assert 2.9 < a.elapsed_time(b) < 50
+    assert B.qi21_check_device_error(ws, ws.numel(), _stream()) == B.QI21_ERR_DEVICE_TIMEOUT
