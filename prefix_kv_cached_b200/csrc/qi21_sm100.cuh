@@ -60,24 +60,22 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull, kSettleNs = 1000000ull;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
                                           uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = globaltimer();
-    bool failed = false;
+    const uint64_t t0 = globaltimer();
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity) && !failed) return true;
-        const uint64_t waited = globaltimer() - t0;
-        if (failed) {
-            if (waited > kSettleNs) return false;
-        } else if (*abort_flag || waited > limit_ns) {
-            if (!*abort_flag) {
-                *abort_flag = 1;
-                raise_device_error(err, DEV_ERR_TIMEOUT);
-            }
-            failed = true;
-            t0 = globaltimer();
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) break;
+        if (globaltimer() - t0 > limit_ns) {
+            *abort_flag = 1;
+            raise_device_error(err, DEV_ERR_TIMEOUT);
+            break;
         }
     }
+    const uint64_t t1 = globaltimer();
+    while (globaltimer() - t1 < kSettleNs) {
+    }
+    return false;
 }
 
 // Failure-path self test: wait on an mbarrier that nothing ever arrives at.
