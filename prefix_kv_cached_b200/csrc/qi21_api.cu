@@ -298,10 +298,18 @@ template <int DH>
 static void launch_attn_tc(Launcher &L, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                            const CUtensorMap &kt, const CUtensorMap &vt, const AttnParams &p, int B) {
     using Cf = AttnCfg<DH>;
-    static DeviceFlags attr;
-    smem_opt_in(k_attn_tc<DH>, (int)Cf::SMEM, attr);
-    dim3 grid((p.Mq + Cf::BQ - 1) / Cf::BQ, p.H, B);
-    L.run("attn", [&] { launch_dep(k_attn_tc<DH>, grid, dim3(Cf::THREADS), Cf::SMEM, L.st, nullptr, q, k, v, kt, vt, p); });
+    const dim3 grid((p.Mq + Cf::BQ - 1) / Cf::BQ, p.H, B);
+    auto go = [&](auto *kernel, DeviceFlags &attr) {
+        smem_opt_in(kernel, (int)Cf::SMEM, attr);
+        L.run("attn", [&] { launch_dep(kernel, grid, dim3(Cf::THREADS), Cf::SMEM, L.st, nullptr, q, k, v, kt, vt, p); });
+    };
+    if (p.shared_tiles > 0) {
+        static DeviceFlags attr;
+        go(k_attn_tc<DH, true>, attr);
+    } else {
+        static DeviceFlags attr;
+        go(k_attn_tc<DH, false>, attr);
+    }
 }
 
 struct TcMaps {
