@@ -568,6 +568,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tmQ, const CUten
     }
     tc_fence_before();
     __syncthreads();
+    settle_if_aborted(abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);

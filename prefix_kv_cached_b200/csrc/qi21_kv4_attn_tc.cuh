@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     tc_fence_before();
     __syncthreads();
+    settle_if_aborted(abort_flag);
     if (warp == 12) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);

@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS, NT == 1 ? 3 : 2) k_kv4_attn_r
         const uint8_t *st = ring.stages + (n % C::STAGES) * C::STAGE;
         const bf16 *kc = kt + (int64_t)(chunk - cp) * KV4R_CHUNK * d, *vc = vt + (int64_t)(chunk - cp) * KV4R_CHUNK * d;
         if (pre) {
-            const bool ok = mbar_wait(smem_u32(&ring.bars[n % C::STAGES]), (n / C::STAGES) & 1, abort_flag, p.err);
+            const bool ok = mbar_wait_settled(smem_u32(&ring.bars[n % C::STAGES]), (n / C::STAGES) & 1, abort_flag, p.err);
             if (!__all_sync(0xffffffffu, ok ? 1 : 0)) break;
         }
         float s[KV4R_M][NT][4];
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(32 * KV4R_WARPS, 4) k_kv4_scores_rows(const __
         for (int m = 0; m < KV4R_M; ++m) sum[m][0] = sum[m][1] = 0.f;
         if (n < n_pre) {
             const uint8_t *st = ring.stages + (n % C::STAGES) * C::STAGE;
-            const bool ok = mbar_wait(smem_u32(&ring.bars[n % C::STAGES]), (n / C::STAGES) & 1, abort_flag, p.err);
+            const bool ok = mbar_wait_settled(smem_u32(&ring.bars[n % C::STAGES]), (n / C::STAGES) & 1, abort_flag, p.err);
             if (!__all_sync(0xffffffffu, ok ? 1 : 0)) break;
             for (int q0 = 0; q0 < p.n_q; q0 += 8) {
                 if (p.n_q > 8) fetch(q0);

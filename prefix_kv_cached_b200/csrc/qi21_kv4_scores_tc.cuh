@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(320, 2)
     }
     tc_fence_before();
     __syncthreads();
+    settle_if_aborted(abort_flag);
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 256);

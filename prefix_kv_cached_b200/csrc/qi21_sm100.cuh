@@ -52,10 +52,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // Bounded wait: returns false (after raising the device error word and the
 // CTA's abort flag) if the phase does not complete within ~2 s, or if another
 // role of the CTA has already aborted. Never traps.
-// A wait that fails returns 1 ms after it gave up: the CTA's copies in flight (loads that
-// nobody waits for any more) take a thousandth of that, and must not land in shared memory
-// that the CTA has left or writes over.
-constexpr uint64_t kWaitLimitNs = 2000000000ull, kSettleNs = 1000000ull;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
                                           uint64_t limit_ns = kWaitLimitNs) {
@@ -65,16 +62,34 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) break;
+        if (*abort_flag) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort_flag = 1;
             raise_device_error(err, DEV_ERR_TIMEOUT);
-            break;
+            return false;
         }
     }
-    const uint64_t t1 = globaltimer();
-    while (globaltimer() - t1 < kSettleNs) {
+}
+
+// After a failed wait: loads that nobody waits for any more must not land in shared memory
+// that the CTA has left or writes over. They get 1 ms, a thousand times what they take.
+// Either at the end of the kernel, once every role has ended (settle_if_aborted), or with
+// the wait itself, where a warp waits for loads of its own; whichever costs a kernel nothing
+// (the other took up to 1.5 % of its time, by the code that it adds).
+constexpr uint64_t kSettleNs = 1000000ull;
+
+__device__ __forceinline__ void settle() {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < kSettleNs) {
     }
+}
+__device__ __forceinline__ void settle_if_aborted(volatile int *abort_flag) {
+    if (*abort_flag) settle();
+}
+__device__ __forceinline__ bool mbar_wait_settled(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                                  uint32_t *err, uint64_t limit_ns = kWaitLimitNs) {
+    if (mbar_wait(bar, parity, abort_flag, err, limit_ns)) return true;
+    settle();
     return false;
 }
 
@@ -90,7 +105,7 @@ __global__ void k_selftest_wait_timeout(uint32_t *err, uint64_t limit_ns) {
         fence_barrier_init();
     }
     __syncthreads();
-    if (threadIdx.x == 0) mbar_wait(smem_u32(&bar), 0, &abort_flag, err, limit_ns);
+    if (threadIdx.x == 0) mbar_wait_settled(smem_u32(&bar), 0, &abort_flag, err, limit_ns);
     __syncthreads();
 }
 
