@@ -180,7 +180,8 @@ class Qi21Runner:
     # ------------------------------------------------------------------ 4-bit prefix cache
 
     def quantise_prefix(self, release: bool = False):
-        """Hold the extracted prefix in 4 bits from here on (for cached_step_kv4). The
+        """Hold the extracted prefix in 4 bits from here on (for cached_step_kv4), in new
+        buffers: a step captured over the ones before must not be replayed any more. The
         extracted cache and its workspace are kept for the next extract, or, with
         release, given back to the allocator: the 4-bit steps do without them, the next
         prefix_extract allocates them again, and a graph of capture_image made before
@@ -234,7 +235,8 @@ class Qi21Runner:
         """Shrink the 4-bit prefix to the `keep` rows of every head that the steps
         with accumulate=True attended to most (the first n_protected rows stay in
         any case). Returns the rows kept, int32 [L][items][H][keep]; the weights
-        start again at zero."""
+        start again at zero. The smaller prefix is in new buffers: a step captured before
+        must not be replayed any more."""
         if self.kv4_scores is None:
             raise ValueError("evict_prefix needs a cached_step_kv4 with accumulate=True before it")
         k = self.kv4
